@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhga.so")
 
 HGA_F32, HGA_BF16 = 0, 1
 HGA_KV_DEVICE, HGA_KV_HOST_PINNED = 0, 1
+HGA_QUANT_E4M3, HGA_QUANT_INT8 = 0, 1
 
 STATUS_NAMES = {0: "HGA_OK", 1: "HGA_ERR_INVALID_ARG", 2: "HGA_ERR_SHAPE", 3: "HGA_ERR_UNSUPPORTED",
                 4: "HGA_ERR_CUDA", 5: "HGA_ERR_TIMEOUT", 6: "HGA_ERR_DEVICE_CHECK",
@@ -30,7 +31,9 @@ SYMBOLS = ("hga_abi_version", "hga_status_string", "hga_last_error", "hga_device
            "hga_gather_warm", "hga_attend_warm", "hga_build_summaries_paged",
            "hga_decode_step_paged", "hga_attend_backward_workspace_size", "hga_attend_backward",
            "hga_cold_open", "hga_cold_close", "hga_cold_write", "hga_cold_stage_bytes",
-           "hga_warm_plan", "hga_cold_stage", "hga_warm_fill")
+           "hga_warm_plan", "hga_cold_stage", "hga_warm_fill",
+           "hga_quant_append", "hga_quant_attend_workspace_size", "hga_quant_attend",
+           "hga_quant_evict")
 
 
 class HGAConfig(ctypes.Structure):
@@ -51,6 +54,16 @@ class HGAKvPages(ctypes.Structure):
 
     _fields_ = [("block_table", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class HGAQuantCache(ctypes.Structure):
+    """Mirror of struct hga_quant_cache (a K/V cache held in 8 bits)."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p),
+                ("v_tail", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("evicted", ctypes.c_void_p), ("n_slots", ctypes.c_int64),
+                ("max_groups", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 class HGAError(RuntimeError):
@@ -74,6 +87,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(HGAConfig)
     KV = ctypes.POINTER(HGAKvPages)
+    QC = ctypes.POINTER(HGAQuantCache)
     sig = {
         "hga_abi_version": (I32, []),
         "hga_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -108,6 +122,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "hga_warm_plan": (ctypes.c_int, [C, I64, P, P, I32, P, P, P, P, P, P, P]),
         "hga_cold_stage": (ctypes.c_int, [P, C, P, P, P, I32, P, I32]),
         "hga_warm_fill": (ctypes.c_int, [C, I64, P, P, P, P, I32, I32, P, P, P]),
+        "hga_quant_append": (ctypes.c_int, [C, QC, P, P, I32, P, P, P, P, P]),
+        "hga_quant_attend_workspace_size": (ctypes.c_int, [C, I32, I32, ctypes.POINTER(SZ)]),
+        "hga_quant_attend": (ctypes.c_int, [C, QC, P, P, P, P, P, P, P, P, SZ, P]),
+        "hga_quant_evict": (ctypes.c_int, [C, QC, P, I32, I32, I32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -403,6 +421,52 @@ def hga_warm_fill(cfg, n_alloc: int, pos, staging, plan, n_plan, warm_groups: in
                                         _ptr(staging), _ptr(plan), _ptr(n_plan), warm_groups,
                                         window_mode, _ptr(k_work), _ptr(v_work), _stream(stream)),
            "hga_warm_fill")
+
+
+def quant_cache(k, v, k_scale, v_scale, k_tail, v_tail, table, n_slots: int, max_groups: int,
+                format: int = HGA_QUANT_E4M3, evicted=None) -> HGAQuantCache:
+    """An 8-bit K/V cache's description (struct hga_quant_cache): pools of n_slots groups, the
+    table [B, Hkv, max_groups] and the tails.  The caller keeps the tensors alive."""
+    return HGAQuantCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
+                         _ptr(v_tail), _ptr(table), _ptr(evicted), n_slots, max_groups, format)
+
+
+def hga_quant_append(cfg, cache: HGAQuantCache, k_new, v_new, n_new: int, pos, counts=None,
+                     chunk_sum=None, group_sum=None, stream=None) -> None:
+    """Writes new rows into an 8-bit cache (tail, closed groups, optional summary rows)."""
+    _check(load_library().hga_quant_append(ctypes.byref(_cfg(cfg)), ctypes.byref(cache),
+                                           _ptr(k_new), _ptr(v_new), n_new, _ptr(counts),
+                                           _ptr(pos), _ptr(chunk_sum), _ptr(group_sum),
+                                           _stream(stream)), "hga_quant_append")
+
+
+def hga_quant_attend_workspace_size(cfg, max_groups: int, weight: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().hga_quant_attend_workspace_size(ctypes.byref(_cfg(cfg)), max_groups,
+                                                          1 if weight else 0, ctypes.byref(out)),
+           "hga_quant_attend_workspace_size")
+    return out.value
+
+
+def hga_quant_attend(cfg, cache: HGAQuantCache, q, pos, out, lse=None, group_idx=None,
+                     weight_in=None, weight_out=None, workspace=None, workspace_bytes: int = 0,
+                     stream=None) -> None:
+    """Decode attention over an 8-bit cache: every live group, or the routed sets of group_idx;
+    weight_out = weight_in + each group's attention weight."""
+    _check(load_library().hga_quant_attend(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _ptr(q),
+                                           _ptr(pos), _ptr(group_idx), _ptr(weight_in),
+                                           _ptr(weight_out), _ptr(out), _ptr(lse),
+                                           _ptr(workspace), workspace_bytes, _stream(stream)),
+           "hga_quant_attend")
+
+
+def hga_quant_evict(cfg, cache: HGAQuantCache, pos, keep: int, sink: int, recent: int, weight_in,
+                    weight_out, table_out, evicted_out, stream=None) -> None:
+    """Keeps the sinks, the newest groups and the heaviest of the others, `keep` in all."""
+    _check(load_library().hga_quant_evict(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _ptr(pos),
+                                          keep, sink, recent, _ptr(weight_in), _ptr(weight_out),
+                                          _ptr(table_out), _ptr(evicted_out), _stream(stream)),
+           "hga_quant_evict")
 
 
 def hga_debug_inject(flags: int) -> int:

@@ -555,6 +555,128 @@ hga_status hga_warm_fill(const hga_config* cfg, int64_t n_alloc, const int64_t* 
   return e == cudaSuccess ? HGA_OK : cuda_fail(e, "hga_warm_fill");
 }
 
+// Checks of an 8-bit cache; p's capacity becomes max_groups * 16 rows.
+static hga_status quant_params(const hga_config* cfg, const hga_quant_cache* cache, LayerParams* p,
+                               QuantCache* out) {
+  hga_status st = make_params(cfg, cfg ? cfg->chunk : 0, 1, p);
+  if (st != HGA_OK) return st;
+  if (cfg->kv_loc != HGA_KV_DEVICE)
+    return fail(HGA_ERR_UNSUPPORTED, "the 8-bit cache lives in device memory");
+  if (!cache || !cache->table) return fail(HGA_ERR_INVALID_ARG, "null cache or table");
+  if (cache->format != HGA_QUANT_E4M3 && cache->format != HGA_QUANT_INT8)
+    return fail(HGA_ERR_INVALID_ARG, "format %d", cache->format);
+  if (cache->max_groups <= 0 || cache->n_slots <= 0)
+    return fail(HGA_ERR_INVALID_ARG, "max_groups and n_slots must be positive");
+  if (cache->max_groups > kQuantMaxGroups || cache->n_slots > 0x7fffffffLL)
+    return fail(HGA_ERR_UNSUPPORTED, "max_groups above %d or n_slots above 2^31 - 1", kQuantMaxGroups);
+  p->n_alloc = static_cast<int64_t>(cache->max_groups) * kQuantGroup;
+  p->n_chunks = static_cast<int>(p->n_alloc / p->C);
+  *out = QuantCache{static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), cache->k_scale,
+                    cache->v_scale, cache->k_tail, cache->v_tail, cache->table, cache->evicted,
+                    cache->n_slots, cache->max_groups, cache->format};
+  return HGA_OK;
+}
+
+static bool aligned16(const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
+
+// The pools and tails, which append and attend read and write in 16-byte pieces.
+static hga_status check_quant_rows(const QuantCache& qc) {
+  if (!qc.k || !qc.v || !qc.k_scale || !qc.v_scale || !qc.k_tail || !qc.v_tail)
+    return fail(HGA_ERR_INVALID_ARG, "null pointer in the cache");
+  if (!aligned16(qc.k) || !aligned16(qc.v) || !aligned16(qc.k_tail) || !aligned16(qc.v_tail))
+    return fail(HGA_ERR_INVALID_ARG, "pools and tails must start on 16-byte boundaries");
+  return HGA_OK;
+}
+
+hga_status hga_quant_append(const hga_config* cfg, const hga_quant_cache* cache, const void* k_new,
+                            const void* v_new, int32_t n_new, const int32_t* counts,
+                            const int64_t* pos, float* chunk_sum, float* group_sum, void* stream) {
+  Range nvtx_range("hga_quant_append");
+  LayerParams p;
+  QuantCache qc;
+  hga_status st = quant_params(cfg, cache, &p, &qc);
+  if (st != HGA_OK) return st;
+  if ((st = check_quant_rows(qc)) != HGA_OK) return st;
+  if (!k_new || !v_new || !pos) return fail(HGA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(k_new) || !aligned16(v_new))
+    return fail(HGA_ERR_INVALID_ARG, "k_new and v_new must start on 16-byte boundaries");
+  if (n_new <= 0) return fail(HGA_ERR_INVALID_ARG, "n_new must be positive");
+  if (!chunk_sum != !group_sum)
+    return fail(HGA_ERR_INVALID_ARG, "chunk_sum and group_sum are given together or not at all");
+  if (chunk_sum && cache->max_groups % p.Ng)
+    return fail(HGA_ERR_SHAPE, "with summary tables, max_groups must be a multiple of chunk / group");
+  unsigned* err = nullptr;
+  if ((st = device_error_ptr(&err)) != HGA_OK) return st;
+  cudaError_t e = launch_quant_append(p, qc, cfg->dtype, k_new, v_new, n_new, counts, pos, chunk_sum,
+                                      group_sum, err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HGA_OK : cuda_fail(e, "hga_quant_append");
+}
+
+hga_status hga_quant_attend_workspace_size(const hga_config* cfg, int32_t max_groups,
+                                           int32_t weight, size_t* bytes) {
+  if (!bytes) return fail(HGA_ERR_INVALID_ARG, "bytes is NULL");
+  LayerParams p;
+  hga_status st = make_params(cfg, cfg ? cfg->chunk : 0, 1, &p);
+  if (st != HGA_OK) return st;
+  if (max_groups <= 0) return fail(HGA_ERR_INVALID_ARG, "max_groups must be positive");
+  if (max_groups > kQuantMaxGroups)
+    return fail(HGA_ERR_UNSUPPORTED, "max_groups above %d", kQuantMaxGroups);
+  *bytes = quant_attend_workspace_bytes(p, max_groups, weight != 0);
+  return HGA_OK;
+}
+
+hga_status hga_quant_attend(const hga_config* cfg, const hga_quant_cache* cache, const void* q,
+                            const int64_t* pos, const int32_t* group_idx, const float* weight_in,
+                            float* weight_out, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  Range nvtx_range("hga_quant_attend");
+  LayerParams p;
+  QuantCache qc;
+  hga_status st = quant_params(cfg, cache, &p, &qc);
+  if (st != HGA_OK) return st;
+  if ((st = check_quant_rows(qc)) != HGA_OK) return st;
+  if (!q || !pos || !out) return fail(HGA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q)) return fail(HGA_ERR_INVALID_ARG, "q must start on a 16-byte boundary");
+  if (!weight_in != !weight_out)
+    return fail(HGA_ERR_INVALID_ARG, "weight_in and weight_out are given together or not at all");
+  if (group_idx && cache->evicted)
+    return fail(HGA_ERR_INVALID_ARG,
+                "routed attention names groups by position: the cache may not have evicted any");
+  const size_t need = quant_attend_workspace_bytes(p, cache->max_groups, weight_out != nullptr);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(HGA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  if (!aligned16(workspace))
+    return fail(HGA_ERR_INVALID_ARG, "the workspace must start on a 16-byte boundary");
+  unsigned* err = nullptr;
+  if ((st = device_error_ptr(&err)) != HGA_OK) return st;
+  cudaError_t e = launch_quant_attend(p, qc, cfg->dtype, cfg->out_dtype, q, pos, group_idx, weight_in,
+                                      weight_out, out, lse, workspace, err,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HGA_OK : cuda_fail(e, "hga_quant_attend");
+}
+
+hga_status hga_quant_evict(const hga_config* cfg, const hga_quant_cache* cache, const int64_t* pos,
+                           int32_t keep, int32_t sink, int32_t recent, const float* weight_in,
+                           float* weight_out, int32_t* table_out, int32_t* evicted_out,
+                           void* stream) {
+  Range nvtx_range("hga_quant_evict");
+  LayerParams p;
+  QuantCache qc;
+  hga_status st = quant_params(cfg, cache, &p, &qc);
+  if (st != HGA_OK) return st;
+  if (!pos || !weight_in || !weight_out || !table_out || !evicted_out)
+    return fail(HGA_ERR_INVALID_ARG, "null pointer");
+  if (sink < 0 || recent < 0 || keep <= 0 || keep - sink < recent)
+    return fail(HGA_ERR_INVALID_ARG, "need keep > 0, sink >= 0, recent >= 0, sink + recent <= keep");
+  if (cache->max_groups > kQuantEvictMax)
+    return fail(HGA_ERR_UNSUPPORTED, "eviction takes at most %d groups", kQuantEvictMax);
+  unsigned* err = nullptr;
+  if ((st = device_error_ptr(&err)) != HGA_OK) return st;
+  cudaError_t e = launch_quant_evict(p, qc, pos, keep, sink, recent, weight_in, weight_out, table_out,
+                                     evicted_out, err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HGA_OK : cuda_fail(e, "hga_quant_evict");
+}
+
 }  // extern "C"
 
 struct hga_cold_store {

@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "quant_cache.cuh"
 
 namespace hga {
 
@@ -231,6 +232,28 @@ cudaError_t launch_attend_prefill_bf16(const LayerParams& p, int out_dtype, cons
                                        const int64_t* pos, const void* k, const void* v,
                                        const int32_t* group_idx, void* out, float* lse,
                                        unsigned* err, cudaStream_t s);
+
+// The 8-bit K/V cache (quant_cache.cuh).  Append: n_new rows [B][Hkv][n_new][D]
+// (the first counts[b] of them, all when counts is null) ending at pos[b];
+// chunk_sum / group_sum both given or both null.
+cudaError_t launch_quant_append(const LayerParams& p, const QuantCache& qc, int dtype,
+                                const void* k_new, const void* v_new, int n_new,
+                                const int32_t* counts, const int64_t* pos, float* chunk_sum,
+                                float* group_sum, unsigned* err, cudaStream_t s);
+size_t quant_attend_workspace_bytes(const LayerParams& p, int max_groups, bool weight);
+// Decode attention over it: every live group (group_idx null) or the routed sets;
+// weight_in / weight_out both given (they may be equal) or both null.
+cudaError_t launch_quant_attend(const LayerParams& p, const QuantCache& qc, int dtype, int out_dtype,
+                                const void* q, const int64_t* pos, const int32_t* group_idx,
+                                const float* weight_in, float* weight_out, void* out, float* lse,
+                                void* ws, unsigned* err, cudaStream_t s);
+// Eviction: at most this many table entries per (sequence, KV head) (one row in
+// shared memory).
+constexpr int kQuantEvictMax = 49152;
+cudaError_t launch_quant_evict(const LayerParams& p, const QuantCache& qc, const int64_t* pos,
+                               int keep, int sink, int recent, const float* weight_in,
+                               float* weight_out, int32_t* table_out, int32_t* evicted_out,
+                               unsigned* err, cudaStream_t s);
 
 // Log-sum-exp merge of nsplit decode partials into out / lse.
 cudaError_t launch_combine(const LayerParams& p, int out_dtype, int nsplit, const float* ws_o,

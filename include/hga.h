@@ -103,6 +103,37 @@ typedef struct hga_kv_pages {
   int32_t max_pages;          /* block-table entries per sequence */
 } hga_kv_pages;
 
+/* Codes of an 8-bit K/V cache: e4m3 (peak 448) or int8 (peak 127). */
+typedef enum hga_quant_format { HGA_QUANT_E4M3 = 0, HGA_QUANT_INT8 = 1 } hga_quant_format;
+
+/*
+ * A K/V cache held in 8 bits (hga_quant_append, hga_quant_attend,
+ * hga_quant_evict), half the bytes of the bf16 cache.  Per (sequence, KV head)
+ * the tokens are groups of 16 (cfg->group); a closed group is one slot of a
+ * pool: 16 x D codes of K and of V and one float32 scale for each, value =
+ * code * scale.  table names, per (sequence, KV head), the slots of its groups
+ * in position order; entries behind the live ones are the item's free slots,
+ * which appends take in order.  No slot may stand in two entries.  The rows of
+ * the open group (the last (pos + 1) % 16 tokens) are kept unrounded in the
+ * tails.  evicted counts the groups hga_quant_evict removed, so the live closed
+ * groups of (b, h) at position pos are (pos + 1) / 16 - evicted[b, h]; NULL:
+ * none was ever evicted.  Positions count every token that was appended.
+ * pos[b] == -1 is a sequence with no tokens.
+ */
+typedef struct hga_quant_cache {
+  void* k;                /* device 8-bit [n_slots, 16, D], 16-byte aligned */
+  void* v;
+  float* k_scale;         /* device [n_slots] */
+  float* v_scale;
+  void* k_tail;           /* device [B, Hkv, 16, D] of cfg->dtype, 16-byte aligned */
+  void* v_tail;
+  const int32_t* table;   /* device [B, Hkv, max_groups] */
+  const int32_t* evicted; /* device [B, Hkv], or NULL */
+  int64_t n_slots;        /* slots in the pool (below 2^31) */
+  int32_t max_groups;     /* table entries per (sequence, KV head), at most 2^20 */
+  int32_t format;         /* hga_quant_format */
+} hga_quant_cache;
+
 /* Version of this ABI (HGA_ABI_VERSION of the built library). */
 int32_t hga_abi_version(void);
 
@@ -540,6 +571,86 @@ hga_status hga_decode_step_paged(const hga_config* cfg, const void* q, const int
                                  const void* v_pages, const hga_kv_pages* kv, int32_t* chunk_idx,
                                  float* chunk_score, int32_t* group_idx, float* group_score,
                                  void* out, float* lse, int32_t append, void* stream);
+
+/*
+ * Writes new tokens into an 8-bit cache: a prompt, a piece of one, or a decode
+ * step's token.  Sequence b gets the first counts[b] of its n_new rows (all of
+ * them when counts is NULL; 0 leaves it as it is, padding rows are not read),
+ * the last of them at position pos[b].  Rows enter the tail; each group they
+ * close is written in 8 bits from its unrounded rows, once, at table entry
+ * (its index) - evicted:
+ *   inverse = peak / amax, scale = amax / peak   (float32, amax = max |x|)
+ *   code = round to nearest even (x * inverse)   (the product rounded to float32)
+ * amax < 2^-100 counts as zero (scale and codes 0); a group holding an infinity
+ * or NaN gets codes 0 and a NaN scale.
+ * With chunk_sum and group_sum (both or neither), the summary rows of the closed
+ * groups, and of the chunks that end with one, are written as
+ * hga_build_summaries writes them, bit for bit, provided the rows of the
+ * chunk's earlier groups stand in group_sum; then n_alloc is max_groups * 16,
+ * max_groups a multiple of C / 16, and a group whose index is max_groups or more
+ * is flagged.
+ *   k_new, v_new  device [B, Hkv, n_new, D] of cfg->dtype (keys post-RoPE)
+ *   counts        device int32 [B], or NULL
+ *   pos           device int64 [B]
+ * A position, count or eviction count that does not fit sets the device error
+ * word and the sequence's (sequence, KV head) is left as it is; a table entry
+ * that is not a slot is flagged and its group is not written.  No workspace.
+ */
+hga_status hga_quant_append(const hga_config* cfg, const hga_quant_cache* cache, const void* k_new,
+                            const void* v_new, int32_t n_new, const int32_t* counts,
+                            const int64_t* pos, float* chunk_sum, float* group_sum, void* stream);
+
+/*
+ * One decode token's exact attention over an 8-bit cache that already holds it
+ * (scale 1/sqrt(D), natural-log LSE, as hga_attend).  With group_idx NULL it
+ * attends every live group and the tail: dense attention, or that of a cache
+ * bounded by hga_quant_evict.  With group_idx (int32 [B, Hkv, kg], as
+ * hga_route writes it) it attends the sets of hga_attend: sink and local
+ * chunks, the current chunk, and the routed groups; cache->evicted must then be
+ * NULL.
+ * With weight_in and weight_out (both or neither, float32 [B, Hkv, max_groups],
+ * equal pointers allowed), weight_out[e] = weight_in[e] + the sum over the G
+ * query heads and the tokens of group e of the attention weights, for every
+ * live entry and for the open group (the entry behind the last closed one);
+ * the entries behind it are left as they are.
+ *   q          device [B, Hq, 1, D] of cfg->dtype, 16-byte aligned
+ *   out        device [B, Hq, 1, D] of cfg->out_dtype
+ *   lse        optional device float32 [B, Hq, 1]
+ *   workspace  device scratch of hga_quant_attend_workspace_size(cfg,
+ *              max_groups, weight_out != NULL) bytes, 16-byte aligned; calls
+ *              that may overlap need their own
+ * A sequence with no tokens gets zeros and an LSE of -inf.  A bad position, table
+ * entry or group id is flagged and skipped as in hga_attend.  Sums are float32;
+ * the softmax weights enter the products with 22 bits, the codes exactly.  The
+ * result does not depend on scheduling.
+ */
+hga_status hga_quant_attend_workspace_size(const hga_config* cfg, int32_t max_groups,
+                                           int32_t weight, size_t* bytes);
+hga_status hga_quant_attend(const hga_config* cfg, const hga_quant_cache* cache, const void* q,
+                            const int64_t* pos, const int32_t* group_idx, const float* weight_in,
+                            float* weight_out, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * Bounds an 8-bit cache: where a (sequence, KV head) has more than `keep` live
+ * closed groups, keeps the first `sink` and the last `recent` of them, and of
+ * those between the keep - sink - recent with the largest accumulated weights
+ * (equal weights: the earlier group; NaN counts as least), all in their order.
+ * Items with at most `keep` groups are passed through.  No key or value
+ * moves: table_out is the row's kept entries, the freed slots, then the slots
+ * that were free, each in order; weight_out is the kept groups' weights, the
+ * open group's, then zeros; evicted_out counts the removed groups up.  Later
+ * calls take a cache with table_out and evicted_out (the position goes on).
+ *   weight_in, weight_out     device float32 [B, Hkv, max_groups]
+ *   table_out, evicted_out    device int32 [B, Hkv, max_groups], [B, Hkv]
+ * Each output may be the array it replaces (in place), and must not overlap it
+ * otherwise.  cache->k .. v_tail are not read and may be NULL.  A bad position is
+ * flagged and its item passed through.  max_groups <= 49152.
+ */
+hga_status hga_quant_evict(const hga_config* cfg, const hga_quant_cache* cache, const int64_t* pos,
+                           int32_t keep, int32_t sink, int32_t recent, const float* weight_in,
+                           float* weight_out, int32_t* table_out, int32_t* evicted_out,
+                           void* stream);
 
 /*
  * hga_attend for callers that cannot allocate device memory.  The paper has no

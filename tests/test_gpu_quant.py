@@ -1,0 +1,649 @@
+"""The 8-bit K/V cache on the GPU: append, attention and eviction against the float64 oracle.
+
+Codes, scales, tails, tables and counts must be equal bit for bit, and the summary rows must be
+hga_build_summaries' bits.  Attention is held to a bound worked out from its arithmetic (see
+`bounds`), so a rounding to fewer bits than the call documents would fail.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU too
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from hierarchical_sparse_attention_hga_b200 import binding as B  # noqa: E402
+from oracle import hga_quant as Q  # noqa: E402
+
+KIND = {"bf16": torch.bfloat16, "f32": torch.float32}
+HGA = {"bf16": B.HGA_BF16, "f32": B.HGA_F32}
+FORM = {"e4m3": B.HGA_QUANT_E4M3, "int8": B.HGA_QUANT_INT8}
+SENTINEL = 0x5A
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from hierarchical_sparse_attention_hga_b200.build import build
+    build()
+    B.load_library()
+
+
+def to_gpu(x, dtype):
+    return torch.as_tensor(np.asarray(x), dtype=torch.float32).to(KIND[dtype]).cuda().contiguous()
+
+
+def stored(x, dtype):
+    """What the GPU sees of x, in float64."""
+    return torch.as_tensor(np.asarray(x), dtype=torch.float32).to(KIND[dtype]).double().numpy()
+
+
+class Cache:
+    """A cache on the GPU, with sentinels where nothing may be written, and its oracle items."""
+
+    def __init__(self, batch, heads_kv, dim, max_groups, dtype="bf16", fmt="e4m3", heads_q=None,
+                 out="f32", seed=0, spare=3, n_slots=None, evicts=False, **layer):
+        self.rng = np.random.default_rng(seed)
+        self.b, self.h, self.d, self.max, self.dtype, self.fmt = batch, heads_kv, dim, max_groups, dtype, fmt
+        self.hq = heads_q or heads_kv
+        bh = batch * heads_kv
+        self.n_slots = n_slots or bh * max_groups + spare
+        order = self.rng.permutation(bh * max_groups + spare) + self.n_slots - (bh * max_groups + spare)
+        self.table = torch.tensor(order[:bh * max_groups].reshape(batch, heads_kv, max_groups), dtype=torch.int32).cuda()
+        self.k = torch.full((self.n_slots, 16, dim), SENTINEL, dtype=torch.uint8, device="cuda")
+        self.v = torch.full_like(self.k, SENTINEL)
+        self.ks = torch.full((self.n_slots,), float("nan"), device="cuda")
+        self.vs = torch.full_like(self.ks, float("nan"))
+        self.kt = torch.full((batch, heads_kv, 16, dim), float("nan"), dtype=KIND[dtype], device="cuda")
+        self.vt = torch.full_like(self.kt, float("nan"))
+        self.evicted = torch.zeros(batch, heads_kv, dtype=torch.int32, device="cuda") if evicts else None
+        self.layer = B.Layer(batch=batch, heads_q=self.hq, heads_kv=heads_kv, head_dim=dim,
+                             dtype=HGA[dtype], out_dtype=HGA[out],
+                             **{"n_high_pairs": dim // 4, **layer})
+        self.out_kind = KIND[out]
+        self.items = [[Q.Item(fmt, dim) for _ in range(heads_kv)] for _ in range(batch)]
+        self.pos = np.full(batch, -1, dtype=np.int64)
+
+    def view(self):
+        return B.quant_cache(self.k, self.v, self.ks, self.vs, self.kt, self.vt, self.table,
+                             self.n_slots, self.max, FORM[self.fmt], self.evicted)
+
+    def pos_t(self):
+        return torch.tensor(self.pos, device="cuda")
+
+    def append(self, k, v, counts=None, gpu=True, **kw):
+        """k, v [B, Hkv, n, D]; counts[b] of them, or all."""
+        n = k.shape[2]
+        c = [n] * self.b if counts is None else counts
+        self.pos = self.pos + np.asarray(c)
+        for b in range(self.b):
+            for h in range(self.h):
+                self.items[b][h].append(stored(k[b, h, :c[b]], self.dtype), stored(v[b, h, :c[b]], self.dtype))
+        if gpu:
+            B.hga_quant_append(self.layer, self.view(), to_gpu(k, self.dtype), to_gpu(v, self.dtype), n,
+                               self.pos_t(), counts=None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda(), **kw)
+
+    def fill(self, lens, spread=1.0):
+        """Sequences of these lengths, appended in one padded call."""
+        n = max(1, max(lens))
+        k = spread * self.rng.standard_normal((self.b, self.h, n, self.d))
+        v = spread * self.rng.standard_normal((self.b, self.h, n, self.d))
+        self.append(k, v, list(lens))
+
+    def check_stored(self):
+        """Every live slot, scale and tail row is the oracle's, and nothing else was touched."""
+        torch.cuda.synchronize()
+        assert B.hga_device_status() == 0
+        table = self.table.cpu().numpy()
+        values = Q.code_values(self.fmt)
+        for codes, scales, tail, name in ((self.k, self.ks, self.kt, "k"), (self.v, self.vs, self.vt, "v")):
+            codes, scales, tail = codes.cpu().numpy(), scales.cpu().numpy(), tail.double().cpu().numpy()
+            live = np.zeros(self.n_slots, bool)
+            for b in range(self.b):
+                for h in range(self.h):
+                    it = self.items[b][h]
+                    for e, (want, scale) in enumerate(getattr(it, name)):
+                        slot = table[b, h, e]
+                        live[slot] = True
+                        np.testing.assert_array_equal(values[codes[slot]], want)
+                        np.testing.assert_array_equal(scales[slot], scale)
+                    rest = getattr(it, name + "_tail")
+                    np.testing.assert_array_equal(tail[b, h, :len(rest)], rest)
+            free = ~live
+            if self.evicted is None:
+                assert (codes[free] == SENTINEL).all() and np.isnan(scales[free]).all()
+
+    def q(self, scale=1.0):
+        return scale * self.rng.standard_normal((self.b, self.hq, 1, self.d))
+
+    def attend(self, q, group_idx=None, weight=None, weight_out=None, ws=None, stream=None):
+        out = torch.full((self.b, self.hq, 1, self.d), 7.0, dtype=self.out_kind, device="cuda")
+        lse = torch.full((self.b, self.hq, 1), 7.0, device="cuda")
+        need = B.hga_quant_attend_workspace_size(self.layer, self.max, weight is not None)
+        if ws is None:  # scratch may hold anything
+            ws = torch.full((max(16, need),), 0xFF, dtype=torch.uint8, device="cuda")
+        B.hga_quant_attend(self.layer, self.view(), to_gpu(q, self.dtype), self.pos_t(), out, lse, group_idx,
+                           weight, weight_out, ws, need, stream=stream)
+        return out, lse
+
+    def check_attend(self, q, got, entries=None, weight_in=None, weight_out=None, flagged=False):
+        out, lse = (t.double().cpu().numpy()[:, :, 0] for t in (got[0], got[1][..., None]))
+        torch.cuda.synchronize()
+        assert B.hga_device_status() == (6 if flagged else 0)
+        g = self.hq // self.h
+        for b in range(self.b):
+            for h in range(self.h):
+                it = self.items[b][h]
+                rows = slice(h * g, h * g + g)
+                qq = stored(q[b, rows, 0], self.dtype)
+                ids = None if entries is None else entries[b][h]
+                want, want_lse, want_weight = it.attend(qq, ids)
+                tol, tol_lse, tol_w = bounds(it, qq, ids, self.out_kind, want, want_lse)
+                err = np.abs(out[b, rows] - want)
+                assert (err <= tol).all(), (b, h, err.max(), np.max(err - tol))
+                if np.isfinite(want_lse).all():
+                    assert (np.abs(lse[b, rows, 0] - want_lse) <= tol_lse).all(), (b, h)
+                else:
+                    np.testing.assert_array_equal(lse[b, rows, 0], want_lse)
+                if weight_in is not None:
+                    n = len(want_weight)
+                    w_in = weight_in[b, h].double().cpu().numpy()
+                    w_got = weight_out[b, h].double().cpu().numpy()
+                    full = w_in[:n] + want_weight
+                    assert (np.abs(w_got[:n] - full) <= tol_w * want_weight + 2.0 ** -23 * np.abs(full) + 1e-30).all()
+                    assert (w_got[n:] == -5).all()
+
+
+def bounds(it, q, entries, out_kind, want, want_lse):
+    """How far the call may be off, from its arithmetic.
+
+    A score is a sum of D products, each of codes (exact in 11 bits) and 22-bit queries, summed in
+    float32 (each addition of the tensor cores within 2^-22 of the largest term), then scaled: off
+    by at most ds = (D + 8) 2^-22 max_t sum_d |q_d k_td| / sqrt(D), plus 2^-22 of the score itself
+    (in the exponent).  A weight is then off by 2 ds relative, plus 2^-20 (the exponential's 2
+    ulp, 22 bits in the product, the scales' roundings).  The sum over T tokens adds T/16 + 64
+    float32 roundings of at most the largest partial sum (each 2^-23).  bfloat16 outputs add half a
+    step."""
+    entries = list(range(len(it.k))) if entries is None else entries
+    k, v = it.rows("k", entries), it.rows("v", entries)
+    if not len(k) or not np.isfinite(want).all():
+        return np.zeros(want.shape), 0.0, 0.0
+    root = np.sqrt(it.dim)
+    size = (np.abs(q) @ np.abs(k).T) / root
+    ds = (it.dim + 8) * 2.0 ** -22 * size.max(1) + 2.0 ** -22 * np.abs(q @ k.T / root).max(1)
+    s = q @ k.T / root
+    p = np.exp(s - want_lse[:, None])
+    mag = p @ np.abs(v)
+    rel = 2 * ds[:, None] + 2.0 ** -20 + (len(k) / 16 + 64) * 2.0 ** -23
+    tol = mag * rel
+    if out_kind is torch.bfloat16:
+        tol = tol + (np.abs(want) + tol) * 2.0 ** -8
+    tol_lse = ds + (len(k) / 16 + 64) * 2.0 ** -23 + 2.0 ** -22 * (1 + np.abs(want_lse))
+    return tol + 1e-37, tol_lse, float(rel.max()) * 2
+
+
+# ---- append
+
+
+@pytest.mark.parametrize("dtype,fmt,dim,chunk,high", [
+    ("bf16", "e4m3", 128, 64, 32), ("bf16", "int8", 64, 128, 0), ("f32", "e4m3", 64, 64, 32),
+    ("f32", "int8", 128, 128, 64)])
+def test_append_in_pieces_equals_one_call_and_the_oracle(dtype, fmt, dim, chunk, high):
+    """A sequence cut into odd pieces: codes, scales and tails are the oracle's, the summary rows
+    hga_build_summaries' bits, whatever the cut."""
+    total = 401
+    per = chunk // 16
+    groups = 32
+    tables = []
+    rng = np.random.default_rng(1)
+    k, v = rng.standard_normal((2, 2, 3, total, dim)) * np.exp(rng.standard_normal(dim))
+    for cut in ([total], [1, 15, 16, 17, 1, 14, 2, 33, 64, 129, 100, 9], [1] * 70 + [total - 70]):
+        c = Cache(2, 3, dim, groups, dtype, fmt, chunk=chunk, n_high_pairs=high)
+        cs = torch.full((2, 3, groups // per, dim), 9.0, device="cuda")
+        gs = torch.full((2, 3, groups // per, per, dim), 9.0, device="cuda")
+        at = 0
+        for n in cut:
+            c.append(k[:, :, at:at + n], v[:, :, at:at + n], chunk_sum=cs, group_sum=gs)
+            at += n
+        assert at == total
+        c.check_stored()
+        tables.append((cs, gs))
+    dense = torch.zeros(2, 3, groups * 16, dim)
+    dense[:, :, :total] = torch.as_tensor(k, dtype=torch.float32)
+    cs, gs = torch.full_like(tables[0][0], 9.0), torch.full_like(tables[0][1], 9.0)
+    B.hga_build_summaries(c.layer, dense.to(KIND[dtype]).cuda(), groups * 16, 0, total, cs, gs)
+    for got in tables:
+        assert torch.equal(got[0], cs) and torch.equal(got[1], gs)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_ragged_counts_and_padding(fmt):
+    """A padded batch: rows behind a sequence's count are NaN and never read, a count of 0 leaves
+    its sequence as it is, also while it holds nothing."""
+    c = Cache(4, 2, 128, 12, fmt=fmt, seed=2)
+    for counts in ([0, 5, 48, 33], [1, 0, 16, 15], [7, 90, 0, 1], [0, 0, 0, 0], [16, 17, 18, 0]):
+        n = 96
+        k, v = c.rng.standard_normal((2, 4, 2, n, 128))
+        for b in range(4):
+            k[b, :, counts[b]:] = v[b, :, counts[b]:] = np.nan
+        c.append(k, v, counts)
+        c.check_stored()
+
+
+def test_append_special_values():
+    """Zeros, values below the cut-off, the largest bfloat16, an infinity and a NaN, each in a
+    group of its own among ordinary ones."""
+    c = Cache(1, 1, 64, 8, "bf16")
+    k, v = c.rng.standard_normal((2, 1, 1, 128, 64))
+    k[0, 0, :16] = 0
+    v[0, 0, 16:32] = 2.0 ** -110
+    k[0, 0, 35, 7] = np.inf
+    v[0, 0, 50, 1] = -np.inf
+    k[0, 0, 70, 3] = np.nan
+    v[0, 0, 80:96] *= 3e37
+    k[0, 0, 96:112] *= 1e-37
+    c.append(k, v)
+    c.check_stored()
+    out, lse = c.attend(c.q())
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_append_flags_what_does_not_fit():
+    c = Cache(3, 2, 128, 4, seed=4, evicts=True)
+    good = c.k.clone()
+    new = c.rng.standard_normal((3, 2, 20, 128))
+    for pos, counts, gone in (([18, 19, 19], None, 0), ([-1, 19, 19], None, 0), ([64, 19, 19], None, 0),
+                              ([19, 19, 19], [21, 20, 20], 0), ([19, 19, 19], [-1, 20, 20], 0),
+                              ([19, 19, 19], None, 1), ([19, 19, 19], None, -1)):
+        c.k.copy_(good)
+        c.evicted.zero_()
+        c.evicted[0] = gone
+        B.hga_quant_append(c.layer, c.view(), to_gpu(new, "bf16"), to_gpu(new, "bf16"), 20, torch.tensor(pos).cuda(),
+                           counts=None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda())
+        assert B.hga_device_status() == 6
+        table = c.table.long().cpu()
+        assert (c.k[table[0].flatten()] == SENTINEL).all()          # sequence 0 untouched
+        assert not (c.k[table[1:, :, 0].flatten()] == SENTINEL).all(1).all(1).any()
+    assert torch.isnan(c.kt[0]).all()
+
+
+def test_append_skips_a_table_entry_that_is_no_slot():
+    c = Cache(1, 2, 128, 4, seed=5)
+    c.table[0, 0, 1] = c.n_slots
+    c.table[0, 1, 0] = -1
+    new = c.rng.standard_normal((1, 2, 64, 128))
+    c.append(new, new)
+    assert B.hga_device_status() == 6
+    done = [(0, 0), (0, 2), (0, 3), (1, 1), (1, 2), (1, 3)]
+    slots = [int(c.table[0, h, e]) for h, e in done]
+    written = (c.k != SENTINEL).flatten(1).any(1).nonzero().flatten().tolist()
+    assert sorted(slots) == written
+    for (h, e), s in zip(done, slots):
+        np.testing.assert_array_equal(Q.code_values("e4m3")[c.k[s].cpu().numpy()], c.items[0][h].k[e][0])
+
+
+# ---- attend
+
+LENS = [0, 1, 15, 16, 17, 31, 100, 257, 640, 1999]
+
+
+@pytest.mark.parametrize("shared", [1, 2, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("dtype,fmt,dim,out", [
+    ("bf16", "e4m3", 128, "f32"), ("bf16", "int8", 128, "bf16"), ("f32", "e4m3", 64, "f32"),
+    ("f32", "int8", 128, "f32"), ("bf16", "int8", 64, "f32"), ("bf16", "e4m3", 64, "bf16")])
+def test_attend_matches_the_oracle(shared, dtype, fmt, dim, out):
+    """Ragged lengths from none to many, NaN in every free slot and free tail row, -1 in the
+    table behind the live entries, with and without weights."""
+    c = Cache(len(LENS), 2, dim, 130, dtype, fmt, heads_q=2 * shared, out=out, seed=shared)
+    c.fill(LENS)
+    for b, n in enumerate(LENS):
+        c.table[b, :, n // 16:] = -1
+    q = c.q(1.5)
+    c.check_attend(q, c.attend(q))
+    w_in = torch.rand(len(LENS), 2, 130, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+    # in place, and the same bits
+    both = w_in.clone()
+    got = c.attend(q, weight=both, weight_out=both)
+    again = c.attend(q)
+    for b, n in enumerate(LENS):
+        m = -(-n // 16)
+        assert torch.equal(both[b, :, :m], w_out[b, :, :m]) and torch.equal(both[b, :, m:], w_in[b, :, m:])
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("batch,heads_kv,lens", [(1, 1, [20000]), (2, 1, [4097, 1]), (40, 8, None), (3, 2, [0, 0, 0])])
+def test_attend_splits_of_every_kind(batch, heads_kv, lens):
+    """One long item over many CTAs, many short ones in one, none at all."""
+    rng = np.random.default_rng(7)
+    lens = lens or [int(x) for x in rng.integers(0, 400, batch)]
+    c = Cache(batch, heads_kv, 128, -(-max(max(lens), 1) // 16) + 1, "bf16", "e4m3", heads_q=4 * heads_kv, seed=8)
+    c.fill(lens)
+    q = c.q()
+    w_in = torch.zeros(batch, heads_kv, c.max, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+    c.check_attend(q, c.attend(q))
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "e4m3"), ("bf16", "int8"), ("f32", "e4m3")])
+def test_attend_uneven_scales(dtype, fmt):
+    """Groups whose K or V are zero, V sizes 2^-40 to 2^40 from group to group, one score far
+    above the others, queries of very different sizes, a zero query."""
+    n = 333
+    c = Cache(2, 2, 128, 24, dtype, fmt, heads_q=12, seed=9)
+    k, v = c.rng.standard_normal((2, 2, 2, n, 128))
+    for g in range(n // 16 + 1):
+        v[:, :, 16 * g:16 * g + 16] *= 2.0 ** c.rng.integers(-40, 41)
+    k[:, :, 32:48] = 0
+    v[:, :, 64:80] = 0
+    v[1] = 0
+    c.append(k, v)
+    q = c.q() * np.logspace(-20, 1, 12)[None, :, None, None]
+    q[0, 3] = 0
+    q[:, 11] = 8 * k[:, 1, 100:101]
+    c.check_attend(q, c.attend(q))
+
+
+def test_attend_tail_values():
+    """Tails of tiny, large and zero rows, beside closed groups and alone."""
+    for dtype in ("bf16", "f32"):
+        c = Cache(4, 1, 64, 4, dtype, heads_q=3, seed=10)
+        k, v = c.rng.standard_normal((2, 4, 1, 27, 64))
+        k[0] *= 1e-25
+        v[1] *= 1e25
+        v[2, 0, 16:] = 0
+        k[3, 0, 20:] *= 50
+        c.append(k, v, [27, 27, 27, 9])
+        q = c.q()
+        c.check_attend(q, c.attend(q))
+
+
+def routed_ids(rng, n, kg, chunk, sink, local):
+    per, cur = chunk // 16, max(0, n - 1) // chunk
+    lo, hi = sink * per, max(0, cur - local) * per
+    m = min(kg, max(0, hi - lo))
+    return sorted(int(g) + lo for g in rng.choice(hi - lo, m, replace=False)) if m else []
+
+
+@pytest.mark.parametrize("chunk,sink,local,kg,shared,dim", [
+    (64, 1, 4, 32, 4, 128), (128, 0, 0, 7, 1, 64), (64, 2, 1, 128, 16, 128), (128, 3, 2, 1, 8, 128)])
+def test_attend_routed_sets(chunk, sink, local, kg, shared, dim):
+    """Sinks, window and routed groups; ids that are -1, not ascending, twice there, in the
+    window or outside the cache are skipped (and all but the -1 flagged)."""
+    lens = [0, 1, 64, 129, 700, 1600, 2040]
+    c = Cache(len(lens), 2, dim, 128, heads_q=2 * shared, seed=11, chunk=chunk, sink_chunks=sink,
+              local_chunks=local, topk_groups=kg)
+    c.fill(lens)
+    idx = np.full((len(lens), 2, kg), -1, np.int32)
+    entries = []
+    for b, n in enumerate(lens):
+        entries.append([])
+        for h in range(2):
+            ids = routed_ids(c.rng, n, kg, chunk, sink, local)
+            idx[b, h, :len(ids)] = ids
+            cur = max(0, n - 1) // chunk
+            per = chunk // 16
+            entries[b].append([g for g in range(n // 16) if g // per < sink or g // per >= cur - local or g in ids])
+    q = c.q()
+    w_in = torch.rand(len(lens), 2, 128, device="cuda")
+    for w in (False, True):
+        w_out = torch.full_like(w_in, -5)
+        kw = dict(weight=w_in, weight_out=w_out) if w else {}
+        got = c.attend(q, torch.tensor(idx).cuda(), **kw)
+        c.check_attend(q, got, entries, *((w_in, w_out) if w else ()))
+    if kg < 7:
+        return
+    bad = idx.copy()
+    for h in range(2):
+        ids = [g for g in bad[6, h] if g >= 0]
+        keep = ids[: kg - 4]
+        row = keep[:2] + [keep[1], 0x7fffffff, 2040 // 16 - 1] + keep[2:]
+        bad[6, h] = (row + [-1] * kg)[:kg]
+        window = [g for g in entries[6][h] if g not in ids]
+        entries[6][h] = sorted(window + keep)
+    got = c.attend(q, torch.tensor(bad).cuda())
+    c.check_attend(q, got, entries, flagged=True)
+
+
+def test_attend_flags_positions_and_slots():
+    """A position that does not fit reads as an empty sequence, a table entry that is no slot is
+    skipped; the other items are right."""
+    c = Cache(4, 2, 128, 10, heads_q=8, seed=12)
+    c.fill([100, 160, 33, 150])
+    q = c.q()
+    right = c.attend(q)
+    saved = c.pos.copy()
+    for bad in (-2, 160, 1 << 40):
+        c.pos = saved.copy()
+        c.pos[1] = bad
+        out, lse = c.attend(q)
+        assert B.hga_device_status() == 6
+        assert not out[1].any() and torch.isneginf(lse[1]).all()
+        assert torch.equal(out[0], right[0][0])
+        np.testing.assert_allclose(out[2:].cpu(), right[0][2:].cpu(), atol=1e-5)
+    c.pos = saved
+    c.table[3, 0, 4] = -7
+    c.table[3, 1, 8] = c.n_slots
+    entries = [[list(range(n // 16)) for _ in range(2)] for n in (100, 160, 33, 150)]
+    entries[3] = [[e for e in range(9) if e != 4], [e for e in range(9) if e != 8]]
+    c.check_attend(q, c.attend(q), entries, flagged=True)
+
+
+def test_attend_a_long_sequence_and_a_pool_past_4_gib():
+    """200,003 tokens in slots behind the first 4 GiB of the pools."""
+    n, dim = 200003, 128
+    groups = n // 16 + 1
+    c = Cache(1, 1, dim, groups, heads_q=4, seed=13, n_slots=(1 << 32) // (16 * dim) + groups + 200)
+    assert int(c.table.min()) * 16 * dim >= 1 << 32
+    c.fill([n])
+    q = c.q(2.0)
+    w_in = torch.zeros(1, 1, groups, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+
+
+# ---- evict
+
+
+def run_evict(c, weight, keep, sink, recent, in_place):
+    w = weight.clone()
+    table, gone = c.table.clone(), c.evicted.clone()
+    outs = (w, table, gone) if in_place else (torch.full_like(w, -5), torch.full_like(table, -5), torch.full_like(gone, -5))
+    v = c.view()
+    if in_place:
+        v = B.quant_cache(None, None, None, None, None, None, table, c.n_slots, c.max, evicted=gone)
+    B.hga_quant_evict(c.layer, v, c.pos_t(), keep, sink, recent, w, *outs)
+    torch.cuda.synchronize()
+    return [t.cpu().numpy() for t in outs]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("max_groups,keep,sink,recent", [
+    (9, 3, 1, 1), (40, 8, 0, 0), (40, 8, 4, 4), (40, 39, 0, 39), (700, 100, 4, 16), (5000, 1, 0, 0),
+    (5000, 1, 0, 1), (5000, 4095, 4, 64)])
+def test_evict_matches_the_oracle(max_groups, keep, sink, recent, in_place):
+    """Ragged numbers of groups (none, fewer than the budget, a full table), many equal weights,
+    NaN, infinities, both zeros and negative ones."""
+    rng = np.random.default_rng(keep + sink)
+    ns = sorted({0, 1, keep, min(keep + 1, max_groups), max_groups // 2, max_groups})
+    for kind in range(3):
+        c = Cache(len(ns), 2, 64, max_groups, seed=14, evicts=True)
+        rest = rng.integers(0, 16, len(ns))
+        gone = rng.integers(0, 9, (len(ns), 1)) * np.ones((1, 2), int)
+        for i, n in enumerate(ns):
+            if n == max_groups:
+                rest[i] = 0
+            c.pos[i] = 16 * (n + gone[i, 0]) + rest[i] - 1
+            if c.pos[i] == -1:
+                gone[i] = 0
+        c.evicted.copy_(torch.tensor(gone))
+        w = rng.standard_normal((len(ns), 2, max_groups)).astype(np.float32)
+        if kind == 1:
+            w = np.round(np.abs(w))                    # few different values
+        if kind == 2:
+            pick = rng.integers(0, 12, w.shape)
+            for i, x in enumerate((np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-42)):
+                w[pick == i] = x
+        got_w, got_t, got_e = run_evict(c, torch.tensor(w).cuda(), keep, sink, recent, in_place)
+        assert B.hga_device_status() == 0
+        table = c.table.cpu().numpy()
+        for b, n in enumerate(ns):
+            for h in range(2):
+                stay = Q.keep_groups(w[b, h], n, keep, sink, recent)
+                freed = [g for g in range(n) if g not in set(stay)]
+                order = stay + freed + list(range(n, max_groups))
+                np.testing.assert_array_equal(got_t[b, h], table[b, h, order])
+                want = np.zeros(max_groups, np.float32)
+                want[:len(stay)] = w[b, h, stay]
+                if n < max_groups:
+                    want[len(stay)] = w[b, h, n]
+                np.testing.assert_array_equal(got_w[b, h], want)
+                assert got_e[b, h] == gone[b, h] + len(freed)
+
+
+def test_evict_largest_table():
+    n = 49152
+    c = Cache(1, 2, 64, n, seed=15, evicts=True)
+    c.pos[0] = 16 * n - 1
+    w = torch.rand(1, 2, n, device="cuda")
+    got_w, got_t, got_e = run_evict(c, w, 30000, 4, 100, True)
+    for h in range(2):
+        stay = np.array(Q.keep_groups(w[0, h].cpu().numpy(), n, 30000, 4, 100))
+        np.testing.assert_array_equal(got_t[0, h, :30000], c.table[0, h].cpu().numpy()[stay])
+        np.testing.assert_array_equal(got_w[0, h, :30000], w[0, h].cpu().numpy()[stay])
+        assert sorted(got_t[0, h]) == sorted(c.table[0, h].tolist()) and got_e[0, h] == n - 30000
+
+
+def test_evict_passes_a_bad_position_through():
+    c = Cache(2, 1, 64, 8, seed=16, evicts=True)
+    c.pos[:] = [8 * 16, 5 * 16 - 1]
+    w = torch.rand(2, 1, 8, device="cuda")
+    got_w, got_t, got_e = run_evict(c, w, 2, 0, 0, False)
+    assert B.hga_device_status() == 6
+    np.testing.assert_array_equal(got_w[0], w[0].cpu())
+    np.testing.assert_array_equal(got_t[0], c.table[0].cpu())
+    assert got_e[0, 0] == 0 and got_e[1, 0] == 3
+
+
+# ---- together
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "e4m3"), ("f32", "int8")])
+def test_a_bounded_decode_loop(dtype, fmt):
+    """Prompts of ragged lengths, then 70 tokens each: append, attend with weights, and a budget
+    of 6 groups held by an eviction after every step.  Every step against the oracle."""
+    keep, sink, recent = 6, 1, 2
+    c = Cache(3, 2, 64, 16, dtype, fmt, heads_q=6, seed=17, evicts=True)
+    c.fill([200, 37, 0])
+    weight = torch.zeros(3, 2, 16, device="cuda")
+    mine = [[np.zeros(16) for _ in range(2)] for _ in range(3)]
+    for step in range(70):
+        new = c.rng.standard_normal((2, 3, 2, 1, 64))
+        c.append(new[0], new[1])
+        q = c.q(1.5)
+        got = c.attend(q, weight=weight, weight_out=weight)
+        c.check_attend(q, got)
+        g = c.hq // c.h
+        for b in range(3):
+            for h in range(2):
+                it = c.items[b][h]
+                w = it.attend(stored(q[b, h * g:h * g + g, 0], dtype))[2]
+                mine[b][h][:len(w)] += w
+                np.testing.assert_allclose(weight[b, h].cpu().numpy(), mine[b][h], rtol=2e-4, atol=1e-5)
+                # the GPU's own sums decide what stays: equal but for rounding
+                n = len(it.k)
+                stay = Q.keep_groups(weight[b, h].cpu().numpy(), n, keep, sink, recent)
+                it.k, it.v = [it.k[i] for i in stay], [it.v[i] for i in stay]
+                tail = mine[b][h][n]
+                mine[b][h] = np.concatenate([mine[b][h][stay], [tail], np.zeros(16 - len(stay) - 1)])
+        B.hga_quant_evict(c.layer, c.view(), c.pos_t(), keep, sink, recent, weight, weight, c.table, c.evicted)
+    # 270, 107 and 70 tokens: 16, 6 and 4 groups
+    assert c.evicted.tolist() == [[10, 10], [0, 0], [0, 0]]
+    c.check_stored()
+
+
+def test_routed_decode_from_the_cache_alone():
+    """No 16-bit cache anywhere: append writes the summaries, hga_route reads them, the attention
+    reads the codes.  The routed ids are those of the bf16 path, the output the oracle's."""
+    n0, steps = 1500, 40
+    c = Cache(2, 2, 128, 100, heads_q=8, seed=18, topk_chunks=4, topk_groups=8, local_chunks=2, n_high_pairs=32)
+    cs = torch.zeros(2, 2, 25, 128, device="cuda")
+    gs = torch.zeros(2, 2, 25, 4, 128, device="cuda")
+    k, v = c.rng.standard_normal((2, 2, 2, n0 + steps, 128))
+    dense = torch.zeros(2, 2, 1600, 128, dtype=torch.bfloat16, device="cuda")
+    dense[:, :, :n0 + steps] = to_gpu(k, "bf16")
+    c.append(k[:, :, :n0], v[:, :, :n0], chunk_sum=cs, group_sum=gs)
+    for t in range(n0, n0 + steps):
+        c.append(k[:, :, t:t + 1], v[:, :, t:t + 1], chunk_sum=cs, group_sum=gs)
+        ci = torch.empty(2, 2, 1, 4, dtype=torch.int32, device="cuda")
+        gi = torch.empty(2, 2, 1, 8, dtype=torch.int32, device="cuda")
+        q = c.q()
+        B.hga_route(c.layer, to_gpu(q, "bf16"), 1, c.pos_t(), cs, gs, 1600, ci, gi)
+        got = c.attend(q, gi)
+        if t % 8 == 0 or t == n0 + steps - 1:
+            cs2, gs2 = torch.zeros_like(cs), torch.zeros_like(gs)
+            B.hga_build_summaries(c.layer, dense, 1600, 0, t + 1, cs2, gs2)
+            ci2, gi2 = torch.empty_like(ci), torch.empty_like(gi)
+            B.hga_route(c.layer, to_gpu(q, "bf16"), 1, c.pos_t(), cs2, gs2, 1600, ci2, gi2)
+            assert torch.equal(gi, gi2)
+            cur = t // 64
+            entries = [[[g for g in range((t + 1) // 16) if g // 4 < 1 or g // 4 >= cur - 2 or g in set(gi[b, h, 0].tolist())]
+                        for h in range(2)] for b in range(2)]
+            c.check_attend(q, got, entries)
+
+
+def test_two_graphs_on_two_streams():
+    """Two captured decode loops, each with its workspace and cache, replayed at the same time
+    with positions advanced on the device; and a graph's replay equals eager calls bit for bit."""
+    runs = []
+    for i in range(2):
+        c = Cache(4, 2, 128, 60, heads_q=8, seed=20 + i, evicts=True)
+        c.fill([300, 17, 640, 0])
+        s = torch.cuda.Stream()
+        pos = c.pos_t()
+        q = to_gpu(c.q(), "bf16")
+        new = to_gpu(c.rng.standard_normal((2, 4, 2, 1, 128)), "bf16")
+        k1, v1 = new[0].contiguous(), new[1].contiguous()
+        w = torch.zeros(4, 2, 60, device="cuda")
+        out, lse = torch.zeros(4, 8, 1, 128, device="cuda"), torch.zeros(4, 8, 1, device="cuda")
+        need = B.hga_quant_attend_workspace_size(c.layer, 60, True)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+        def step(c=c, pos=pos, q=q, k1=k1, v1=v1, w=w, out=out, lse=lse, ws=ws, need=need):
+            pos.add_(1)
+            B.hga_quant_append(c.layer, c.view(), k1, v1, 1, pos)
+            B.hga_quant_attend(c.layer, c.view(), q, pos, out, lse, None, w, w, ws, need)
+            B.hga_quant_evict(c.layer, c.view(), pos, 12, 1, 2, w, w, c.table, c.evicted)
+
+        state = [pos, w, out, lse, c.table, c.evicted, c.k, c.v, c.ks, c.vs, c.kt, c.vt]
+        runs.append((s, step, state, [t.clone() for t in state]))
+    torch.cuda.synchronize()
+    graphs = []
+    for s, step, state, before in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for (s, step, state, before) in runs:
+        for t, x in zip(state, before):
+            t.copy_(x)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for g, (s, *_r) in zip(graphs, runs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    after = [[t.clone() for t in state] for _, _, state, _ in runs]
+    for (s, step, state, before), want in zip(runs, after):
+        for t, x in zip(state, before):
+            t.copy_(x)
+        for _ in range(40):
+            step()
+        torch.cuda.synchronize()
+        for t, x in zip(state, want):
+            assert torch.equal(torch.nan_to_num(t.float()), torch.nan_to_num(x.float()))
+    assert B.hga_device_status() == 0
