@@ -111,7 +111,7 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
         const bool some = finite && amax >= 0x1p-100f;
         const float inverse = some ? __fdiv_rn(kPeak, amax) : 0.f;
         const float scale = some ? __fdiv_rn(amax, kPeak) : (finite ? 0.f : CUDART_NAN_F);
-        const int32_t slot = __ldg(qc.table + item * qc.max_groups + (u - gone));
+        const int32_t slot = qc.table[item * qc.max_groups + (u - gone)];
         if (slot >= 0 && slot < qc.n_slots) {
           uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * PPL;
 #pragma unroll

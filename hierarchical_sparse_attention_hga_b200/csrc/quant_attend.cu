@@ -3,9 +3,37 @@
 // One query token per sequence attends, exactly, every live group of its
 // (sequence, KV head) and the open group's tail rows, or, given routed group
 // ids, the sinks, the window and the routed groups (the sets of hga_attend):
-//   s_t = (q . c_t) * k_scale / sqrt(D),  p = softmax(s),  out = sum_t p_t v_scale c'_t
+//   s_t = (q . c_t) k_scale / sqrt(D),  p = softmax(s),  out = sum_t p_t v_scale c'_t
 // with codes c, c'.  On request each group's weight, the sum of p over its
 // tokens and the G query heads of the KV head, is added to an accumulator.
+//
+// Bound by HBM: 2 D bytes a token are read once, for 4 G D operations.  So the
+// codes go from global memory straight into registers, in the very bytes that
+// the matrix instruction's operand layout wants from each lane, are widened
+// there to f16 (exact for both formats) and multiplied on mma.sync m16n8k16 with
+// the TOKENS as the 16 rows and the query heads as the 8 columns: no shared
+// memory, no wasted rows for few heads.  S^T = K Q^T lands with a lane holding
+// two heads of two tokens; movmatrix turns it into the second product's operand
+// (O^T += V^T P^T).  The order in which the D dimensions meet in a product is
+// free as long as both operands agree, and so is the order of O's rows; both are
+// chosen so that a lane's bytes are 16 consecutive ones of a row.
+//
+// Precision.  bf16 queries, scaled by a power of two, are exact in f16; float32
+// ones are split into a high and a low half.  The softmax weights, multiplied by
+// v_scale, are split into two halves as well (22 bits): with at most four heads
+// the low halves take the unused four columns, for free.  References of the
+// running softmax are integers, so every rescaling is exact, and v_scale enters
+// as exponent and mantissa, so its size never costs bits.  Each tile's product
+// starts from zero and is added to the running sum in float32 (round to
+// nearest): the matrix unit's own accumulation is never longer than a tile.
+//
+// Work.  A fixed grid; the units (groups, and one for a tail) of all items form
+// one list, of which each CTA takes an equal slice, whatever the sequences'
+// lengths.  A CTA leaves one partial (sum, reference, denominator) per item it
+// touches, at slot CTA + item (distinct, since one of the two grows from each
+// partial to the next); a second kernel merges them, in a fixed order.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_cache.cuh"
@@ -13,15 +41,108 @@
 namespace hga {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kGMax = 16;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 2;             // units a warp works on at a time
+constexpr int kMinSlice = kWarps * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -1e30f;     // reference before the first score
+constexpr float kHeadroom = 2.f;     // a raised reference exceeds the maximum by 2 to 3
+constexpr float kWeightExp = 14.f;   // weights are at most 2 * 2^(14 - 2) in f16
 
-// Table entries a query attends, as a virtual list: [0, a_end), then
-// [b_base, closed), then the routed ids (kept ones; -1 where an entry is not).
+// Resident CTAs per SM that the register use allows.
+__host__ __device__ constexpr int ctas_per_sm(int gm) { return gm == 16 ? 2 : 3; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of halves held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Streaming loads: every byte of the pool is read once per call.
+__device__ __forceinline__ void load_stream(const uint8_t* p, uint32_t (&r)[4]) {
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+}
+__device__ __forceinline__ void load_stream(const uint8_t* p, uint32_t (&r)[2]) {
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+}
+
+// Four codes as two pairs of halves: exact.  int8: 1024 + (code + 128) is a half
+// whose low byte is code + 128; subtracting 1152 leaves the code.
+template <int FORMAT>
+__device__ __forceinline__ void widen4(uint32_t r, uint32_t& lo, uint32_t& hi) {
+  if (FORMAT == kQuantE4m3) {
+    lo = e4m3x2_to_half2(static_cast<uint16_t>(r));
+    hi = e4m3x2_to_half2(static_cast<uint16_t>(r >> 16));
+  } else {
+    const uint32_t x = r ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+    const __half2 hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&ha);
+    hi = *reinterpret_cast<const uint32_t*>(&hb);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The remainder of (a, b) that pack_half2 left, as halves.
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_half2(a - f.x, b - f.y);
+}
+
+// 2^n for an integer n in [-126, 127].
+__device__ __forceinline__ float exp2i(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+
+// Exponent e (clamped to [-100, 127]) of the largest finite |value|'s bits, so
+// that value * 2^(14 - e) is below 2^15; 0 for all-zero input.
+__device__ __forceinline__ int scale_exponent(uint32_t top_bits) {
+  return top_bits == 0 ? 0 : max(static_cast<int>(top_bits >> 23) - 127, -100);
+}
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+
+// v_scale as mant * 2^ex.
+__device__ __forceinline__ void split_scale(float v, float& mant, float& ex) {
+  const uint32_t u = __float_as_uint(v), e = (u >> 23) & 255;
+  if (e == 0) {  // zero or subnormal
+    mant = v * 0x1p126f;
+    ex = -126.f;
+  } else if (e == 255) {
+    mant = v;
+    ex = 0.f;
+  } else {
+    mant = __uint_as_float((u & 0x807fffffu) | 0x3f800000u);
+    ex = static_cast<float>(static_cast<int>(e) - 127);
+  }
+}
+
+// The units a query attends, as a virtual list: groups [0, a_end), groups
+// [b_base, closed), the routed ids (entries that are not kept: -1), the tail.
 struct Units {
-  int a_end, b_base, fixed, total;
+  int a_end, b_base, fixed, groups, total;
   __device__ __forceinline__ int entry(int i, const int* routed) const {
     if (i < a_end) return i;
     if (i < fixed) return b_base + (i - a_end);
@@ -29,179 +150,824 @@ struct Units {
   }
 };
 
-template <typename T, int D, int FORMAT, typename TO>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ Units units_of(const LayerParams& p, const QuantItem& it, int64_t pos,
+                                          bool routed) {
+  Units u{0, 0, it.closed, it.closed, it.units()};
+  if (routed && u.total) {
+    const int first = max(0, static_cast<int>(pos / p.C) - p.local);
+    u.a_end = min(p.sink, first) * p.Ng;
+    u.b_base = first * p.Ng;
+    u.fixed = u.a_end + it.closed - u.b_base;
+    u.groups = u.fixed + p.kg;
+    u.total = u.groups + (it.rest > 0);
+  }
+  return u;
+}
+
+// Scratch of one call.
+struct Workspace {
+  int2* parts;     // [items]: first CTA of the item, number of CTAs
+  float* stat;     // [ctas + items][16][4]: weight reference, score reference, denominator
+  float* sum;      // [ctas + items][G][D], dimensions in the kernel's order
+  float2* group;   // [items][G][max_groups + kg]: each unit's sum (-1: a routed id that is not
+                   // kept) and its reference, in the virtual list's order (weights only)
+};
+
+// The dimension at place i of a partial sum's row.
+template <int D>
+__device__ __forceinline__ int dim_of(int i) {
+  return ((i >> 1) & 7) * (D / 8) + 2 * (i >> 4) + (i & 1);
+}
+
+// GM: query heads per KV head rounded up to 4, 8 or 16.
+template <typename T, int D, int FORMAT, int GM>
+struct Warp {
+  static constexpr int NT = GM == 16 ? 2 : 1;          // 8-column tiles
+  static constexpr int NK = D / 16;                    // k-steps, and 16-row tiles of O^T
+  static constexpr bool kSplitQ = sizeof(T) == 4;      // a low half of the queries
+
+  uint32_t qh[NT][NK][2], ql[kSplitQ ? NT : 1][kSplitQ ? NK : 1][2];
+  float f[NT][2];                                      // score scale of this lane's columns (log2 units)
+  float o[NK][NT][4];
+  float ref_w[NT][2], ref_s[NT][2], l[NT][2];
+
+  // Query heads of (b, h): column n of tile nt is head nt * 8 + n; with GM == 4
+  // columns 4..7 repeat heads 0..3.
+  __device__ __forceinline__ void load_q(const T* q, const LayerParams& p, int b, int h) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int head = GM == 4 ? g & 3 : nt * 8 + g;
+      float x[NK][4];
+      uint32_t top = 0;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        if (head < p.G)
+          load4(q + (static_cast<int64_t>(b) * p.Hq + h * p.G + head) * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, x[ks]);
+        else
+          x[ks][0] = x[ks][1] = x[ks][2] = x[ks][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, finite_bits(x[ks][i]));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = scale_exponent(top);
+      const float up = exp2i(14 - e);
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[ks][i] *= up;
+        qh[nt][ks][0] = pack_half2(x[ks][0], x[ks][1]);
+        qh[nt][ks][1] = pack_half2(x[ks][2], x[ks][3]);
+        if constexpr (kSplitQ) {
+          ql[nt][ks][0] = pack_rest(x[ks][0], x[ks][1], qh[nt][ks][0]);
+          ql[nt][ks][1] = pack_rest(x[ks][2], x[ks][3], qh[nt][ks][1]);
+        }
+      }
+      const float down = exp2i(e - 14) * (kLog2e * rsqrtf(static_cast<float>(D)));
+      f[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);       // column 2c is lane group g = 2c
+      f[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+    }
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ref_w[nt][e] = ref_s[nt][e] = kNoRef;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < NK; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+    }
+  }
+
+  // Softmax of U units' scores x (log2 units, -inf where there is no token):
+  // raises the references if need be, adds to l, and leaves the weights times
+  // v_scale (mant * 2^ex) as operands pb[u][nt][high, low][2].  group != null:
+  // the sum of p per unit and head goes to group[head * stride + at[u]] (at >= 0).
+  template <int U>
+  __device__ __forceinline__ void softmax(const float (&x)[U][NT][4], const float (&mant)[U],
+                                          const float (&ex)[U], uint32_t (&pb)[U][NT][2][2],
+                                          float2* group, int stride, const int (&at)[U],
+                                          const bool (&kept)[U], int G) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    float top_s[NT][2], top_w[NT][2];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float a = -CUDART_INF_F, b = -CUDART_INF_F;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float y = fmaxf(x[u][nt][e], x[u][nt][e + 2]);
+          a = fmaxf(a, y);
+          b = fmaxf(b, y + ex[u]);
+        }
+        top_s[nt][e] = a;
+        top_w[nt][e] = b;
+        raise |= a > ref_s[nt][e] || b > ref_w[nt][e];
+      }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float a = top_s[nt][e], b = top_w[nt][e];
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
+          }
+          const float na = a > ref_s[nt][e] ? ceilf(a) + kHeadroom : ref_s[nt][e];
+          const float nb = b > ref_w[nt][e] ? ceilf(b) + kHeadroom : ref_w[nt][e];
+          l[nt][e] *= ex2(ref_s[nt][e] - na);
+          const float corr = ex2(ref_w[nt][e] - nb);  // integers: exact
+#pragma unroll
+          for (int mt = 0; mt < NK; ++mt) {
+            o[mt][nt][e] *= corr;
+            o[mt][nt][e + 2] *= corr;
+          }
+          ref_s[nt][e] = na;
+          ref_w[nt][e] = nb;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4], sum[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p0 = ex2(x[u][nt][e] - ref_s[nt][e]), p1 = ex2(x[u][nt][e + 2] - ref_s[nt][e]);
+          sum[e] = p0 + p1;
+          l[nt][e] += sum[e];
+          const float r = ref_w[nt][e] - kWeightExp - ex[u];
+          w[e] = mant[u] * ex2(x[u][nt][e] - r);
+          w[e + 2] = mant[u] * ex2(x[u][nt][e + 2] - r);
+        }
+        const uint32_t h0 = pack_half2(w[0], w[1]), h1 = pack_half2(w[2], w[3]);
+        const uint32_t r0 = pack_rest(w[0], w[1], h0), r1 = pack_rest(w[2], w[3], h1);
+        if constexpr (GM == 4) {  // columns 0..3: high halves, 4..7: low halves
+          pb[u][nt][0][0] = transpose8(c < 2 ? h0 : r0);
+          pb[u][nt][0][1] = transpose8(c < 2 ? h1 : r1);
+        } else {
+          pb[u][nt][0][0] = transpose8(h0);
+          pb[u][nt][0][1] = transpose8(h1);
+          pb[u][nt][1][0] = transpose8(r0);
+          pb[u][nt][1][1] = transpose8(r1);
+        }
+        if (group) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float s = sum[e];
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+            const int head = nt * 8 + 2 * c + e;
+            if (g == 0 && head < G && at[u] >= 0 && (GM != 4 || c < 2))
+              group[static_cast<int64_t>(head) * stride + at[u]] =
+                  make_float2(kept[u] ? s : -1.f, ref_s[nt][e]);
+          }
+        }
+      }
+  }
+
+  // Tail rows (rest of them valid) as one unit.
+  __device__ void tail(const T* kt, const T* vt, int rest, float2* group, int stride, int unit, int G) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    float x[1][NT][4];
+    int e_k, e_v;
+    {
+      float k[2][NK][4];
+      uint32_t top = 0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+          if (g + 8 * r < rest)
+            load_row(kt + (g + 8 * r) * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, k[r][ks]);
+          else
+            k[r][ks][0] = k[r][ks][1] = k[r][ks][2] = k[r][ks][3] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, finite_bits(k[r][ks][i]));
+        }
+      e_k = scale_exponent(__reduce_max_sync(0xffffffffu, top));
+      const float up = exp2i(14 - e_k);
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k[r][ks][i] *= up;
+          a[r] = pack_half2(k[r][ks][0], k[r][ks][1]);
+          a[r + 2] = pack_half2(k[r][ks][2], k[r][ks][3]);
+          b[r] = pack_rest(k[r][ks][0], k[r][ks][1], a[r]);
+          b[r + 2] = pack_rest(k[r][ks][2], k[r][ks][3], a[r + 2]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma(s[nt], a[0], a[1], a[2], a[3], qh[nt][ks][0], qh[nt][ks][1]);
+          if constexpr (kSplitQ) {
+            mma(s[nt], a[0], a[1], a[2], a[3], ql[nt][ks][0], ql[nt][ks][1]);
+            mma(s[nt], b[0], b[1], b[2], b[3], qh[nt][ks][0], qh[nt][ks][1]);
+          }
+        }
+      }
+      const float down = exp2i(e_k - 14);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float fs = f[nt][i & 1] * down;
+          x[0][nt][i] = g + 8 * (i >> 1) < rest ? s[nt][i] * fs : -CUDART_INF_F;
+        }
+    }
+    // V: rows 2c, 2c + 1, 2c + 8, 2c + 9, this lane's D / 8 dimensions
+    float v[4][D / 8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+      for (int j = 0; j < D / 8; j += 4) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (row < rest) load_row(vt + row * D + g * (D / 8) + j, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[r][j + i] = y[i];
+          top = max(top, finite_bits(y[i]));
+        }
+      }
+    }
+    e_v = scale_exponent(__reduce_max_sync(0xffffffffu, top));
+    const float up = exp2i(14 - e_v);
+    const float mant[1] = {1.f}, ex[1] = {static_cast<float>(e_v - 14)};
+    const int at[1] = {unit};
+    const bool kept[1] = {true};
+    uint32_t pb[1][NT][2][2];
+    softmax<1>(x, mant, ex, pb, group, stride, at, kept, G);
+#pragma unroll
+    for (int mt = 0; mt < NK; ++mt) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const float y0 = v[2 * r][2 * mt + d] * up, y1 = v[2 * r + 1][2 * mt + d] * up;
+          a[2 * r + d] = pack_half2(y0, y1);
+          b[2 * r + d] = pack_rest(y0, y1, a[2 * r + d]);
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        mma(s, a[0], a[1], a[2], a[3], pb[0][nt][0][0], pb[0][nt][0][1]);
+        if constexpr (GM != 4) mma(s, a[0], a[1], a[2], a[3], pb[0][nt][1][0], pb[0][nt][1][1]);
+        if constexpr (kSplitQ) mma(s, b[0], b[1], b[2], b[3], pb[0][nt][0][0], pb[0][nt][0][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][nt][i] += s[i];
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void load_row(const float* p, float (&y)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
+  }
+  static __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&y)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    y[0] = __uint_as_float(v.x << 16); y[1] = __uint_as_float(v.x & 0xffff0000u);
+    y[2] = __uint_as_float(v.y << 16); y[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+
+// One tile's codes and scales on their way into registers.
+template <int D>
+struct Raw {
+  uint32_t k[kTile][2][D / 64][4];      // rows g, g + 8; 16 bytes at 64 j + 16 c
+  uint32_t v[kTile][4][D / 32];         // rows 2c, 2c + 1, 2c + 8, 2c + 9; D / 8 bytes at g D / 8
+  float ks[kTile], vs[kTile];
+  int slot[kTile];                      // -1: no unit
+  int entry[kTile];
+};
+
+template <typename T, int D, int FORMAT, int GM>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(GM))
 quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
                     const int64_t* __restrict__ pos, const int32_t* __restrict__ group_idx,
-                    const float* weight_in, float* weight_out, TO* __restrict__ out,
-                    float* __restrict__ lse, float* __restrict__ ws, unsigned* err) {
-  __shared__ float s_k[kQuantGroup][D + 1], s_v[kQuantGroup][D + 1];
-  __shared__ float s_q[kGMax][D + 1];
-  __shared__ float s_p[kGMax][kQuantGroup], s_m[kGMax], s_l[kGMax], s_scale[kGMax];
-  extern __shared__ int s_routed[];
+                    Workspace ws, unsigned* err) {
+  using W = Warp<T, D, FORMAT, GM>;
+  constexpr int NT = W::NT, NK = W::NK;
+  constexpr int kRow = D + 8;  // padded row of the merge buffer
+  extern __shared__ int s_routed[];  // [kg] of the current item
+  __shared__ float s_sum[kWarps][GM][kRow];
+  __shared__ float s_stat[kWarps][GM][3];
+  __shared__ int64_t s_part[kThreads];
+  __shared__ int64_t s_start;
+  __shared__ int s_item;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
+  pdl_wait();
+
+  auto item_units = [&](int64_t i, unsigned* e) {
+    const int64_t pb = pos[i / p.Hkv];
+    return units_of(p, quant_item(qc, pb, i, e), pb, group_idx != nullptr).total;
+  };
+  // where this CTA's slice [lo, hi) of all units begins
+  const int64_t per = (items + kThreads - 1) / kThreads;
+  const int64_t i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
+  int64_t mine = 0;
+  for (int64_t i = i_lo; i < i_hi; ++i) mine += item_units(i, blockIdx.x == 0 ? err : nullptr);
+  s_part[tid] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t v[kThreads / 32], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kThreads / 32; ++j) {
+      v[j] = s_part[lane * (kThreads / 32) + j];
+      sum += v[j];
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    int64_t run = x - sum;
+#pragma unroll
+    for (int j = 0; j < kThreads / 32; ++j) {
+      s_part[lane * (kThreads / 32) + j] = run;
+      run += v[j];
+    }
+    if (lane == 31) s_start = x;  // all units
+  }
+  __syncthreads();
+  const int64_t all = s_start;
+  int64_t slice = (all + gridDim.x - 1) / gridDim.x;
+  slice = max(static_cast<int64_t>(kMinSlice), (slice + kTile - 1) / kTile * kTile);
+  const int64_t lo = slice * blockIdx.x, hi = min(all, lo + slice);
+  if (lo >= hi) return;
+  __syncthreads();
+  if (s_part[tid] <= lo && lo < s_part[tid] + mine) {
+    int64_t at = s_part[tid];
+    int64_t i = i_lo;
+    for (;; ++i) {
+      const int n = item_units(i, nullptr);
+      if (lo < at + n) break;
+      at += n;
+    }
+    s_item = static_cast<int>(i);
+    s_start = at;
+  }
+  __syncthreads();
+  int64_t item = s_item, start = s_start;
+
+  W w;
+  for (int64_t next = lo; next < hi; ++item) {
+    const int b = static_cast<int>(item / p.Hkv), h = static_cast<int>(item % p.Hkv);
+    const int64_t pb = pos[b];
+    const QuantItem it = quant_item(qc, pb, item, nullptr);
+    const Units un = units_of(p, it, pb, group_idx != nullptr);
+    if (un.total == 0) continue;
+    const int u_lo = static_cast<int>(next - start);
+    const int u_hi = static_cast<int>(min(hi - start, static_cast<int64_t>(un.total)));
+    if (tid == 0 && u_lo == 0) {
+      const int64_t last = (start + un.total - 1) / slice;
+      ws.parts[item] = make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
+    }
+    if (un.groups > un.fixed) {
+      // kept: ids of candidate chunks, larger than all candidate ids before them
+      __syncthreads();
+      if (warp == 0) {
+        const int32_t* ids = group_idx + item * p.kg;
+        const int first = un.b_base / p.Ng;
+        int before = -1;
+        bool bad = false;
+        for (int i0 = 0; i0 < p.kg; i0 += 32) {
+          const int id = i0 + lane < p.kg ? ids[i0 + lane] : -1;
+          const bool candidate = id >= 0 && id / p.Ng >= p.sink && id / p.Ng < first;
+          int m = candidate ? id : -1;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, y);
+          }
+          int prev = __shfl_up_sync(0xffffffffu, m, 1);
+          prev = max(before, lane ? prev : -1);
+          const bool keep = candidate && id > prev;
+          bad |= id >= 0 && !keep;
+          if (i0 + lane < p.kg) s_routed[i0 + lane] = keep ? id : -1;
+          before = max(before, __shfl_sync(0xffffffffu, m, 31));
+        }
+        if (bad) flag_error(err, kErrGroupIdx);
+      }
+      __syncthreads();
+    }
+    const int stride = qc.max_groups + p.kg;
+    float2* group = ws.group ? ws.group + item * p.G * stride : nullptr;
+    const int32_t* table = qc.table + item * qc.max_groups;
+    const int g_hi = min(u_hi, un.groups);  // groups of the slice: [u_lo, g_hi)
+
+    // table entries of the warp's tile at unit u
+    auto load_slots = [&](int u, int (&slot)[kTile], int (&entry)[kTile]) {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        entry[j] = u + j < g_hi ? un.entry(u + j, s_routed) : -1;
+        slot[j] = -1;
+        if (entry[j] >= 0) {
+          slot[j] = table[entry[j]];
+          if (slot[j] < 0 || slot[j] >= qc.n_slots) {
+            if (lane == 0) flag_error(err, kErrPage);
+            slot[j] = -1;
+          }
+        }
+      }
+    };
+    Raw<D> raw;
+    auto load_k = [&]() {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        if (raw.slot[j] >= 0) {
+          const uint8_t* base = qc.k + static_cast<int64_t>(raw.slot[j]) * (kQuantGroup * D) + g * D + c * 16;
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) load_stream(base + r * 8 * D + i * 64, raw.k[j][r][i]);
+          raw.ks[j] = qc.k_scale[raw.slot[j]];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+              raw.k[j][r][i][0] = raw.k[j][r][i][1] = raw.k[j][r][i][2] = raw.k[j][r][i][3] = 0u;
+          raw.ks[j] = 0.f;
+        }
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        if (raw.slot[j] >= 0) {
+          const uint8_t* base = qc.v + static_cast<int64_t>(raw.slot[j]) * (kQuantGroup * D) + 2 * c * D + g * (D / 8);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) load_stream(base + ((r & 1) + 8 * (r >> 1)) * D, raw.v[j][r]);
+          raw.vs[j] = qc.v_scale[raw.slot[j]];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw.v[j][r][i] = 0u;
+          raw.vs[j] = 0.f;
+        }
+      }
+    };
+
+    int u = u_lo + warp * kTile;
+    constexpr int kStep = kWarps * kTile;
+    int slot_next[kTile], entry_next[kTile];
+    load_slots(u, raw.slot, raw.entry);
+    load_slots(u + kStep, slot_next, entry_next);
+    load_k();
+    load_v();
+    w.load_q(q, p, b, h);
+    w.clear();
+    for (; u < g_hi; u += kStep) {
+      float x[kTile][NT][4], mant[kTile], ex[kTile];
+      int at[kTile];
+      bool kept[kTile];
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+          uint32_t a0, a1, a2, a3;
+          widen4<FORMAT>(raw.k[j][0][ks >> 2][ks & 3], a0, a2);
+          widen4<FORMAT>(raw.k[j][1][ks >> 2][ks & 3], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(x[j][nt], a0, a1, a2, a3, w.qh[nt][ks][0], w.qh[nt][ks][1]);
+            if constexpr (W::kSplitQ) mma(x[j][nt], a0, a1, a2, a3, w.ql[nt][ks][0], w.ql[nt][ks][1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[j][nt][i] = raw.slot[j] >= 0 ? x[j][nt][i] * (w.f[nt][i & 1] * raw.ks[j]) : -CUDART_INF_F;
+        split_scale(raw.vs[j], mant[j], ex[j]);
+        at[j] = u + j < g_hi ? u + j : -1;
+        kept[j] = raw.entry[j] >= 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        raw.slot[j] = slot_next[j];
+        raw.entry[j] = entry_next[j];
+      }
+      load_k();
+      load_slots(u + 2 * kStep, slot_next, entry_next);
+      uint32_t pb[kTile][NT][2][2];
+      w.template softmax<kTile>(x, mant, ex, pb, group, stride, at, kept, p.G);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t a[kTile][2][4];  // the two 16-row tiles of these four bytes
+#pragma unroll
+        for (int j = 0; j < kTile; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t lo16 = __byte_perm(raw.v[j][2 * r][i], raw.v[j][2 * r + 1][i], 0x5140);
+            const uint32_t hi16 = __byte_perm(raw.v[j][2 * r][i], raw.v[j][2 * r + 1][i], 0x7362);
+            widen4<FORMAT>(lo16, a[j][0][2 * r], a[j][0][2 * r + 1]);
+            widen4<FORMAT>(hi16, a[j][1][2 * r], a[j][1][2 * r + 1]);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) {
+              const uint32_t(&y)[4] = a[j][half];
+              mma(s, y[0], y[1], y[2], y[3], pb[j][nt][0][0], pb[j][nt][0][1]);
+              if constexpr (GM != 4) mma(s, y[0], y[1], y[2], y[3], pb[j][nt][1][0], pb[j][nt][1][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[2 * i + half][nt][e] += s[e];
+          }
+      }
+      load_v();
+    }
+
+    if (u_hi > un.groups && warp == kWarps - 1) {
+      const int64_t at = item * kQuantGroup * D;
+      w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
+             stride, un.groups, p.G);
+    }
+
+    // merge the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) w.l[nt][e] += __shfl_xor_sync(0xffffffffu, w.l[nt][e], k);
+        const int head = nt * 8 + 2 * c + e;
+#pragma unroll
+        for (int mt = 0; mt < NK; ++mt) {
+          float y0 = w.o[mt][nt][e], y1 = w.o[mt][nt][e + 2];
+          if constexpr (GM == 4) {
+            y0 += __shfl_xor_sync(0xffffffffu, y0, 2);
+            y1 += __shfl_xor_sync(0xffffffffu, y1, 2);
+          }
+          if (GM != 4 || c < 2)
+            *reinterpret_cast<float2*>(&s_sum[warp][head][mt * 16 + g * 2]) = make_float2(y0, y1);
+        }
+        if (g == 0 && (GM != 4 || c < 2)) {
+          s_stat[warp][head][0] = w.ref_w[nt][e];
+          s_stat[warp][head][1] = w.ref_s[nt][e];
+          s_stat[warp][head][2] = w.l[nt][e];
+        }
+      }
+    __syncthreads();
+    const int64_t part = blockIdx.x + item;
+    for (int i = tid; i < p.G * D; i += kThreads) {
+      const int head = i / D, d = i % D;
+      float ref = s_stat[0][head][0];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) ref = fmaxf(ref, s_stat[k][head][0]);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) sum += s_sum[k][head][d] * ex2(s_stat[k][head][0] - ref);
+      ws.sum[(part * p.G + head) * D + d] = sum;
+    }
+    if (tid < p.G) {
+      float rw = kNoRef, rs = kNoRef, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        rw = fmaxf(rw, s_stat[k][tid][0]);
+        rs = fmaxf(rs, s_stat[k][tid][1]);
+      }
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) l += s_stat[k][tid][2] * ex2(s_stat[k][tid][1] - rs);
+      *reinterpret_cast<float4*>(ws.stat + (part * 16 + tid) * 4) = make_float4(rw, rs, l, 0.f);
+    }
+    __syncthreads();
+    start += un.total;
+    next = start;
+  }
+  pdl_trigger();
+}
+
+// Merges an item's partials.  Block y < G: query head y's output and LSE; block
+// y >= G: the weights of 1024 table entries.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeEntries = 1024;
+template <int D, typename TO>
+__global__ void __launch_bounds__(kMergeThreads)
+quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos, Workspace ws,
+                   const int32_t* __restrict__ group_idx, const float* weight_in,
+                   float* weight_out, TO* __restrict__ out,
+                   float* __restrict__ lse) {
+  constexpr int kMergeWarps = kMergeThreads / 32;
+  __shared__ float s_sum[kMergeWarps][D];
+  __shared__ float s_l[kMergeWarps];
+  __shared__ float s_ref[16][2];
+  __shared__ float s_add[kMergeEntries];
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv), h = static_cast<int>(item % p.Hkv);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int64_t pb = pos[b];
-  const QuantItem it = quant_item(qc, pb, item, tid == 0 ? err : nullptr);
-  Units un{0, 0, it.closed, it.closed};
-  if (group_idx && it.units()) {
-    const int cur = static_cast<int>(pb / p.C);
-    const int first = max(0, cur - p.local);
-    un.a_end = min(p.sink, first) * p.Ng;
-    un.b_base = first * p.Ng;
-    un.fixed = un.a_end + it.closed - un.b_base;
-    un.total = un.fixed + p.kg;
-    for (int i = tid; i < p.kg; i += kThreads) s_routed[i] = group_idx[item * p.kg + i];
-    __syncthreads();
-    if (tid == 0) {
-      int prev = -1;
-      bool bad = false;
-      for (int i = 0; i < p.kg; ++i) {
-        const int id = s_routed[i];
-        if (id < 0) { s_routed[i] = -1; continue; }
-        const int c = id / p.Ng;
-        if (c < p.sink || c >= first || id <= prev) { bad = true; s_routed[i] = -1; continue; }
-        prev = id;
-      }
-      if (bad) flag_error(err, kErrGroupIdx);
+  const QuantItem it = quant_item(qc, pos[b], item, nullptr);
+  const int units = it.units();
+  const int2 parts = units ? ws.parts[item] : make_int2(0, 0);
+  const int64_t first = parts.x + item;
+  const float4* stat = reinterpret_cast<const float4*>(ws.stat) + first * 16;
+  const int y = blockIdx.y;
+  if (y < p.G) {
+    float rw = kNoRef, rs = kNoRef;
+    for (int i = lane; i < parts.y; i += 32) {
+      const float4 s = stat[i * 16 + y];
+      rw = fmaxf(rw, s.x);
+      rs = fmaxf(rs, s.y);
     }
-  }
-  const float scale = kLog2e * rsqrtf(static_cast<float>(D));
-  for (int i = tid; i < p.G * D; i += kThreads)
-    s_q[i / D][i % D] = to_f32(q[(static_cast<int64_t>(b) * p.Hq + h * p.G) * D + i]) * scale;
-  if (tid < kGMax) { s_m[tid] = -CUDART_INF_F; s_l[tid] = 0.f; }
-  __syncthreads();
-  float* lu = ws + item * p.G * qc.max_groups;  // log2 of each group's sum, per query head
-  if (weight_out)
-    for (int i = tid; i < p.G * qc.max_groups; i += kThreads) lu[i] = -CUDART_INF_F;
-  float acc[kGMax];
+    rw = warp_max(rw);
+    rs = warp_max(rs);
+    float acc[D / 32], l = 0.f;
 #pragma unroll
-  for (int j = 0; j < kGMax; ++j) acc[j] = 0.f;
-  const int d = tid % D;
-  constexpr int HS = kThreads / D;
-  for (int u = 0; u < un.total + (it.rest > 0); ++u) {
-    const bool tail = u == un.total;
-    const int e = tail ? it.closed : un.entry(u, s_routed);
-    __syncthreads();
-    if (e < 0) continue;
-    int rows = kQuantGroup;
-    if (tail) {
-      rows = it.rest;
-      const T* kt = static_cast<const T*>(qc.k_tail) + item * kQuantGroup * D;
-      const T* vt = static_cast<const T*>(qc.v_tail) + item * kQuantGroup * D;
-      for (int i = tid; i < rows * D; i += kThreads) {
-        s_k[i / D][i % D] = to_f32(kt[i]);
-        s_v[i / D][i % D] = to_f32(vt[i]);
-      }
-    } else {
-      const int32_t slot = qc.table[item * qc.max_groups + e];
-      if (slot < 0 || slot >= qc.n_slots) {
-        if (tid == 0) flag_error(err, kErrPage);
-        continue;
-      }
-      const int64_t base = static_cast<int64_t>(slot) * kQuantGroup * D;
-      const float ks = qc.k_scale[slot], vs = qc.v_scale[slot];
-      for (int i = tid; i < kQuantGroup * D; i += kThreads) {
-        s_k[i / D][i % D] = code_to_f32<FORMAT>(qc.k[base + i]) * ks;
-        s_v[i / D][i % D] = code_to_f32<FORMAT>(qc.v[base + i]) * vs;
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < p.G * kQuantGroup; i += kThreads) {
-      const int hh = i / kQuantGroup, t = i % kQuantGroup;
-      float s = -CUDART_INF_F;
-      if (t < rows) {
-        s = 0.f;
-        for (int x = 0; x < D; ++x) s += s_q[hh][x] * s_k[t][x];
-      }
-      s_p[hh][t] = s;
-    }
-    __syncthreads();
-    if (tid < p.G) {
-      float m = s_m[tid], mu = -CUDART_INF_F, sum = 0.f;
-      for (int t = 0; t < rows; ++t) mu = fmaxf(mu, s_p[tid][t]);
-      const float mn = fmaxf(m, mu), ref = mn == -CUDART_INF_F ? 0.f : mn;
-      for (int t = 0; t < rows; ++t) {
-        const float x = exp2f(s_p[tid][t] - ref);
-        s_p[tid][t] = x;
-        sum += x;
-      }
-      s_scale[tid] = m == -CUDART_INF_F ? 0.f : exp2f(m - ref);
-      s_l[tid] = s_l[tid] * s_scale[tid] + sum;
-      s_m[tid] = mn;
-      if (weight_out) lu[tid * qc.max_groups + e] = log2f(sum) + ref;
-    }
-    __syncthreads();
+    for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < parts.y; i += kMergeWarps) {
+      const float4 s = stat[i * 16 + y];
+      const float* row = ws.sum + ((first + i) * p.G + y) * D;
+      const float f = ex2(s.x - rw);
+      l += s.z * ex2(s.y - rs);
 #pragma unroll
-    for (int j = 0; j < kGMax; ++j) {
-      const int hh = tid / D + j * HS;
-      if (hh >= p.G) continue;
-      acc[j] *= s_scale[hh];
-      for (int t = 0; t < rows; ++t) acc[j] += s_p[hh][t] * s_v[t][d];
+      for (int j = 0; j < D / 32; ++j) acc[j] += f * row[j * 32 + lane];
     }
-  }
-  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kGMax; ++j) {
-    const int hh = tid / D + j * HS;
-    if (hh >= p.G) continue;
-    const float m = s_m[hh], l = s_l[hh];
-    const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + hh;
-    store_out(out + row * D + d, l == 0.f ? 0.f : acc[j] / l);
-    if (lse && d == 0) lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
-  }
-  if (weight_out) {
-    for (int e = tid; e < it.units(); e += kThreads) {
-      float sum = 0.f;
-      for (int hh = 0; hh < p.G; ++hh)
-        if (s_l[hh] != 0.f) sum += exp2f(lu[hh * qc.max_groups + e] - (s_m[hh] + log2f(s_l[hh])));
-      const int64_t at = item * qc.max_groups + e;
-      weight_out[at] = weight_in[at] + sum;
+    for (int j = 0; j < D / 32; ++j) s_sum[warp][j * 32 + lane] = acc[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (tid < D) {
+      float sum = 0.f, den = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) {
+        sum += s_sum[k][tid];
+        den += s_l[k];
+      }
+      const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + y;
+      // sum is in units of 2^(rw - 14), den in units of 2^rs
+      store_out(out + row * D + dim_of<D>(tid), den == 0.f ? 0.f : sum / den * ex2(rw - kWeightExp - rs));
+      if (lse && tid == 0) lse[row] = den == 0.f ? -CUDART_INF_F : (rs + log2f(den)) * kLn2;
+    }
+  } else {
+    const int e0 = (y - p.G) * kMergeEntries;
+    if (e0 < units) {
+      for (int head = warp; head < p.G; head += kMergeWarps) {
+        float rs = kNoRef, l = 0.f;
+        for (int i = lane; i < parts.y; i += 32) rs = fmaxf(rs, stat[i * 16 + head].y);
+        rs = warp_max(rs);
+        for (int i = lane; i < parts.y; i += 32) {
+          const float4 s = stat[i * 16 + head];
+          l += s.z * ex2(s.y - rs);
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+          s_ref[head][0] = rs;
+          s_ref[head][1] = l == 0.f ? 0.f : 1.f / l;
+        }
+      }
+      __syncthreads();
+      const Units un = units_of(p, it, pos[b], group_idx != nullptr);
+      const int stride = qc.max_groups + p.kg;
+      auto unit_weight = [&](int u) {
+        float sum = 0.f;
+        for (int head = 0; head < p.G; ++head) {
+          const float2 s = ws.group[(item * p.G + head) * stride + u];
+          sum += s.x * ex2(s.y - s_ref[head][0]) * s_ref[head][1];
+        }
+        return sum;
+      };
+      const int e1 = min(units, e0 + kMergeEntries);
+      if (un.groups > un.fixed) {  // the routed ids of these entries
+        for (int i = tid; i < kMergeEntries; i += kMergeThreads) s_add[i] = 0.f;
+        __syncthreads();
+        for (int i = tid; i < p.kg; i += kMergeThreads) {
+          const int id = group_idx[item * p.kg + i];
+          if (id >= e0 && id < e1 && ws.group[item * p.G * stride + un.fixed + i].x != -1.f)
+            s_add[id - e0] = unit_weight(un.fixed + i);
+        }
+        __syncthreads();
+      }
+      for (int e = e0 + tid; e < e1; e += kMergeThreads) {
+        float sum;
+        if (e == it.closed) sum = unit_weight(un.groups);
+        else if (e < un.a_end) sum = unit_weight(e);
+        else if (e >= un.b_base) sum = unit_weight(un.a_end + e - un.b_base);
+        else sum = s_add[e - e0];
+        const int64_t at = item * qc.max_groups + e;
+        weight_out[at] = weight_in[at] + sum;
+      }
     }
   }
   pdl_trigger();
 }
 
-template <typename T, int D, int FORMAT, typename TO>
-cudaError_t launch_t(const LayerParams& p, const QuantCache& qc, const void* q, const int64_t* pos,
-                     const int32_t* group_idx, const float* weight_in, float* weight_out, void* out,
-                     float* lse, void* ws, unsigned* err, cudaStream_t s) {
-  return launch_pdl(quant_attend_kernel<T, D, FORMAT, TO>, dim3(static_cast<unsigned>(p.B * p.Hkv)),
-                    dim3(kThreads), static_cast<size_t>(group_idx ? p.kg : 0) * sizeof(int), s, 1, p,
-                    qc, static_cast<const T*>(q), pos, group_idx, weight_in, weight_out,
-                    static_cast<TO*>(out), lse, static_cast<float*>(ws), err);
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int heads_rounded(const LayerParams& p) { return p.G <= 4 ? 4 : p.G <= 8 ? 8 : 16; }
+
+// Scratch layout; base may be null (sizes only).
+size_t layout(const LayerParams& p, int max_groups, bool weight, char* base, Workspace* ws) {
+  const size_t items = static_cast<size_t>(p.B) * p.Hkv;
+  const size_t parts = items + static_cast<size_t>(device_sm_count()) * ctas_per_sm(heads_rounded(p));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* x = base + at;
+    at += align256(bytes);
+    return x;
+  };
+  ws->stat = reinterpret_cast<float*>(take(parts * 16 * 4 * sizeof(float)));
+  ws->sum = reinterpret_cast<float*>(take(parts * p.G * p.D * sizeof(float)));
+  ws->parts = reinterpret_cast<int2*>(take(items * sizeof(int2)));
+  ws->group = nullptr;
+  if (weight)
+    ws->group = reinterpret_cast<float2*>(take(items * p.G * (static_cast<size_t>(max_groups) + p.kg) * sizeof(float2)));
+  return at;
 }
 
-template <typename T, int D>
-cudaError_t launch_f(const LayerParams& p, const QuantCache& qc, int out_dtype, const void* q,
-                     const int64_t* pos, const int32_t* group_idx, const float* wi, float* wo,
-                     void* out, float* lse, void* ws, unsigned* err, cudaStream_t s) {
-  using bf = __nv_bfloat16;
+template <typename T, int D, int FORMAT, int GM>
+cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void* q, const int64_t* pos,
+                          const int32_t* group_idx, const Workspace& ws, unsigned* err, cudaStream_t s) {
+  // at most the resident CTAs, and no more than the largest possible list has slices
+  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
+  int64_t most = qc.max_groups;
+  if (group_idx) most = std::min(most, static_cast<int64_t>(p.sink + p.local + 1) * p.Ng) + p.kg + 1;
+  const int64_t slices = (items * most + kMinSlice - 1) / kMinSlice;
+  const int64_t resident = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(GM);
+  const unsigned grid = static_cast<unsigned>(slices < resident ? slices : resident);
+  return launch_pdl(quant_attend_kernel<T, D, FORMAT, GM>, dim3(grid), dim3(kThreads),
+                    group_idx ? p.kg * sizeof(int) : 0, s, 1, p, qc, static_cast<const T*>(q), pos,
+                    group_idx, ws, err);
+}
+
+template <typename T, int D, int FORMAT>
+cudaError_t launch_g(const LayerParams& p, const QuantCache& qc, const void* q, const int64_t* pos,
+                     const int32_t* gi, const Workspace& ws, unsigned* err, cudaStream_t s) {
+  switch (heads_rounded(p)) {
+    case 4: return launch_attend<T, D, FORMAT, 4>(p, qc, q, pos, gi, ws, err, s);
+    case 8: return launch_attend<T, D, FORMAT, 8>(p, qc, q, pos, gi, ws, err, s);
+    default: return launch_attend<T, D, FORMAT, 16>(p, qc, q, pos, gi, ws, err, s);
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const LayerParams& p, const QuantCache& qc, const void* q, const int64_t* pos,
+                     const int32_t* gi, const Workspace& ws, unsigned* err, cudaStream_t s) {
   if (qc.format == kQuantInt8)
-    return out_dtype == 0 ? launch_t<T, D, kQuantInt8, float>(p, qc, q, pos, group_idx, wi, wo, out, lse, ws, err, s)
-                          : launch_t<T, D, kQuantInt8, bf>(p, qc, q, pos, group_idx, wi, wo, out, lse, ws, err, s);
-  return out_dtype == 0 ? launch_t<T, D, kQuantE4m3, float>(p, qc, q, pos, group_idx, wi, wo, out, lse, ws, err, s)
-                        : launch_t<T, D, kQuantE4m3, bf>(p, qc, q, pos, group_idx, wi, wo, out, lse, ws, err, s);
+    return p.D == 64 ? launch_g<T, 64, kQuantInt8>(p, qc, q, pos, gi, ws, err, s)
+                     : launch_g<T, 128, kQuantInt8>(p, qc, q, pos, gi, ws, err, s);
+  return p.D == 64 ? launch_g<T, 64, kQuantE4m3>(p, qc, q, pos, gi, ws, err, s)
+                   : launch_g<T, 128, kQuantE4m3>(p, qc, q, pos, gi, ws, err, s);
+}
+
+template <int D, typename TO>
+cudaError_t launch_merge(const LayerParams& p, const QuantCache& qc, const int64_t* pos,
+                         const Workspace& ws, const int32_t* group_idx, const float* weight_in,
+                         float* weight_out, void* out, float* lse, cudaStream_t s) {
+  const int blocks = weight_out ? (qc.max_groups + kMergeEntries - 1) / kMergeEntries : 0;
+  return launch_pdl(quant_merge_kernel<D, TO>, dim3(static_cast<unsigned>(p.B * p.Hkv), p.G + blocks),
+                    dim3(kMergeThreads), 0, s, 1, p, qc, pos, ws, group_idx, weight_in, weight_out,
+                    static_cast<TO*>(out), lse);
 }
 
 }  // namespace
 
 size_t quant_attend_workspace_bytes(const LayerParams& p, int max_groups, bool weight) {
-  return weight ? static_cast<size_t>(p.B) * p.Hq * max_groups * sizeof(float) : 0;
+  Workspace ws;
+  return layout(p, max_groups, weight, nullptr, &ws);
 }
 
 cudaError_t launch_quant_attend(const LayerParams& p, const QuantCache& qc, int dtype, int out_dtype,
                                 const void* q, const int64_t* pos, const int32_t* group_idx,
                                 const float* weight_in, float* weight_out, void* out, float* lse,
-                                void* ws, unsigned* err, cudaStream_t s) {
+                                void* workspace, unsigned* err, cudaStream_t s) {
   using bf = __nv_bfloat16;
-  if (dtype == 0)
-    return p.D == 64 ? launch_f<float, 64>(p, qc, out_dtype, q, pos, group_idx, weight_in, weight_out, out, lse, ws, err, s)
-                     : launch_f<float, 128>(p, qc, out_dtype, q, pos, group_idx, weight_in, weight_out, out, lse, ws, err, s);
-  return p.D == 64 ? launch_f<bf, 64>(p, qc, out_dtype, q, pos, group_idx, weight_in, weight_out, out, lse, ws, err, s)
-                   : launch_f<bf, 128>(p, qc, out_dtype, q, pos, group_idx, weight_in, weight_out, out, lse, ws, err, s);
+  Workspace ws;
+  layout(p, qc.max_groups, weight_out != nullptr, static_cast<char*>(workspace), &ws);
+  cudaError_t e = dtype == 0 ? launch_t<float>(p, qc, q, pos, group_idx, ws, err, s)
+                             : launch_t<bf>(p, qc, q, pos, group_idx, ws, err, s);
+  if (e != cudaSuccess) return e;
+  if (p.D == 64)
+    return out_dtype == 0 ? launch_merge<64, float>(p, qc, pos, ws, group_idx, weight_in, weight_out, out, lse, s)
+                          : launch_merge<64, bf>(p, qc, pos, ws, group_idx, weight_in, weight_out, out, lse, s);
+  return out_dtype == 0 ? launch_merge<128, float>(p, qc, pos, ws, group_idx, weight_in, weight_out, out, lse, s)
+                        : launch_merge<128, bf>(p, qc, pos, ws, group_idx, weight_in, weight_out, out, lse, s);
 }
 
 }  // namespace hga
