@@ -7,16 +7,18 @@
 // with codes c, c'.  On request each group's weight, the sum of p over its
 // tokens and the G query heads of the KV head, is added to an accumulator.
 //
-// Bound by HBM: 2 D bytes a token are read once, for 4 G D operations.  So the
-// codes go from global memory straight into registers, in the very bytes that
-// the matrix instruction's operand layout wants from each lane, are widened
-// there to f16 (exact for both formats) and multiplied on mma.sync m16n8k16 with
-// the TOKENS as the 16 rows and the query heads as the 8 columns: no shared
-// memory, no wasted rows for few heads.  S^T = K Q^T lands with a lane holding
+// Bound by HBM: 2 D bytes a token are read once, for 4 G D operations.  Each warp
+// streams groups through a ring of its own in shared memory (16-byte
+// asynchronous copies, each 512 contiguous bytes a warp), reads the codes back in
+// the very bytes that the matrix instruction's operand layout wants from each
+// lane, widens them in registers to f16 (exact for both formats) and multiplies
+// on mma.sync m16n8k16 with the TOKENS as the 16 rows and the query heads as the
+// 8 columns: no wasted rows for few heads.  S^T = K Q^T lands with a lane holding
 // two heads of two tokens; movmatrix turns it into the second product's operand
 // (O^T += V^T P^T).  The order in which the D dimensions meet in a product is
-// free as long as both operands agree, and so is the order of O's rows; both are
-// chosen so that a lane's bytes are 16 consecutive ones of a row.
+// free as long as both operands agree, and so are the orders of a group's tokens
+// and of O's rows; they are chosen so that a lane's bytes are consecutive ones of
+// a row and no two lanes of a phase meet in a bank (see Tile).
 //
 // Precision.  bf16 queries, scaled by a power of two, are exact in f16; float32
 // ones are split into a high and a low half.  The softmax weights, multiplied by
@@ -29,7 +31,8 @@
 //
 // Work.  A fixed grid; the units (groups, and one for a tail) of all items form
 // one list, of which each CTA takes an equal slice, whatever the sequences'
-// lengths.  A CTA leaves one partial (sum, reference, denominator) per item it
+// lengths.  Every item stands there with kItemCost more units than it has, for
+// what it costs beside its bytes.  A CTA leaves one partial (sum, reference, denominator) per item it
 // touches, at slot CTA + item (distinct, since one of the two grows from each
 // partial to the next); a second kernel merges them, in a fixed order.
 #include <algorithm>
@@ -44,6 +47,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 2;             // units a warp works on at a time
+constexpr int kStages = 2;           // tiles in a warp's ring
+constexpr int kItemCost = 16;        // an item's fixed work, in units (see the slices)
 constexpr int kMinSlice = kWarps * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -74,14 +79,42 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Streaming loads: every byte of the pool is read once per call.
-__device__ __forceinline__ void load_stream(const uint8_t* p, uint32_t (&r)[4]) {
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+// 16 bytes from global to shared memory; zeros when !valid (nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void load_stream(const uint8_t* p, uint32_t (&r)[2]) {
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&r)[2]) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+
+// One unit's codes in shared memory: K rows, then V rows, D bytes each, with the
+// 16-byte pieces of row r permuted by an XOR.  Row n of the matrix products is
+// token token(n), so that
+//  - K: the two rows that eight lanes read (n = 2m, 2m + 1; 64 bytes of each) lie
+//    in different halves of the banks,
+//  - V: the four rows (n = 2c, or 2c + 1) and the neighbouring pieces that a
+//    phase's lanes read cover every bank once.
+template <int D>
+struct Tile {
+  static constexpr int kUnitBytes = 2 * kQuantGroup * D;
+  static __device__ __forceinline__ int token(int n) {
+    const int c = (n & 7) >> 1, even = D == 128 ? 2 * c : c;
+    return (n & 8) | ((n & 1) ? even ^ 5 : even);
+  }
+  static __device__ __forceinline__ int piece(int row, int i) {
+    return row * D + ((i ^ (D == 128 ? row & 7 : row & 2)) << 4);
+  }
+};
 
 // Four codes as two pairs of halves: exact.  int8: 1024 + (code + 128) is a half
 // whose low byte is code + 128; subtracting 1152 leaves the code.
@@ -346,8 +379,9 @@ struct Warp {
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
-          if (g + 8 * r < rest)
-            load_row(kt + (g + 8 * r) * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, k[r][ks]);
+          const int row = g + 8 * r;
+          if (row < rest)
+            load_row(kt + row * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, k[r][ks]);
           else
             k[r][ks][0] = k[r][ks][1] = k[r][ks][2] = k[r][ks][3] = 0.f;
 #pragma unroll
@@ -446,16 +480,6 @@ struct Warp {
   }
 };
 
-// One tile's codes and scales on their way into registers.
-template <int D>
-struct Raw {
-  uint32_t k[kTile][2][D / 64][4];      // rows g, g + 8; 16 bytes at 64 j + 16 c
-  uint32_t v[kTile][4][D / 32];         // rows 2c, 2c + 1, 2c + 8, 2c + 9; D / 8 bytes at g D / 8
-  float ks[kTile], vs[kTile];
-  int slot[kTile];                      // -1: no unit
-  int entry[kTile];
-};
-
 template <typename T, int D, int FORMAT, int GM>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(GM))
 quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
@@ -464,25 +488,35 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
   using W = Warp<T, D, FORMAT, GM>;
   constexpr int NT = W::NT, NK = W::NK;
   constexpr int kRow = D + 8;  // padded row of the merge buffer
-  extern __shared__ int s_routed[];  // [kg] of the current item
-  __shared__ float s_sum[kWarps][GM][kRow];
+  constexpr int kUnitBytes = Tile<D>::kUnitBytes;
+  constexpr int kRing = kStages * kTile * kUnitBytes;
+  static_assert(GM * kRow * 4 <= kRing, "a warp's partial sum reuses its ring");
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // [kWarps][kRing], then [kg] routed ids
+  int* s_routed = reinterpret_cast<int*>(s_dyn + kWarps * kRing);
+  __shared__ float s_scale[kWarps][kStages][kTile][2];  // k_scale, v_scale
+  __shared__ int s_state[kWarps][kStages][kTile];       // 1: in the ring, 0: no tokens, -1: id not kept
   __shared__ float s_stat[kWarps][GM][3];
   __shared__ int64_t s_part[kThreads];
   __shared__ int64_t s_start;
   __shared__ int s_item;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = s_dyn + warp * kRing;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint32_t scale_at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_scale[warp][0][0][0]));
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
   pdl_wait();
 
-  auto item_units = [&](int64_t i, unsigned* e) {
+  // an item's length in the list of all items' units, its fixed work in front
+  auto item_length = [&](int64_t i, unsigned* e) {
     const int64_t pb = pos[i / p.Hkv];
-    return units_of(p, quant_item(qc, pb, i, e), pb, group_idx != nullptr).total;
+    const int n = units_of(p, quant_item(qc, pb, i, e), pb, group_idx != nullptr).total;
+    return n ? n + kItemCost : 0;
   };
-  // where this CTA's slice [lo, hi) of all units begins
+  // where this CTA's slice [lo, hi) of the list begins
   const int64_t per = (items + kThreads - 1) / kThreads;
   const int64_t i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
   int64_t mine = 0;
-  for (int64_t i = i_lo; i < i_hi; ++i) mine += item_units(i, blockIdx.x == 0 ? err : nullptr);
+  for (int64_t i = i_lo; i < i_hi; ++i) mine += item_length(i, blockIdx.x == 0 ? err : nullptr);
   s_part[tid] = mine;
   __syncthreads();
   if (warp == 0) {
@@ -504,7 +538,7 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
       s_part[lane * (kThreads / 32) + j] = run;
       run += v[j];
     }
-    if (lane == 31) s_start = x;  // all units
+    if (lane == 31) s_start = x;  // the whole list
   }
   __syncthreads();
   const int64_t all = s_start;
@@ -517,7 +551,7 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
     int64_t at = s_part[tid];
     int64_t i = i_lo;
     for (;; ++i) {
-      const int n = item_units(i, nullptr);
+      const int n = item_length(i, nullptr);
       if (lo < at + n) break;
       at += n;
     }
@@ -534,10 +568,12 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
     const QuantItem it = quant_item(qc, pb, item, nullptr);
     const Units un = units_of(p, it, pb, group_idx != nullptr);
     if (un.total == 0) continue;
-    const int u_lo = static_cast<int>(next - start);
-    const int u_hi = static_cast<int>(min(hi - start, static_cast<int64_t>(un.total)));
+    const int64_t first = start + kItemCost, end = first + un.total;
+    if (hi <= first) break;  // only the item's fixed part
+    const int u_lo = static_cast<int>(max(next - first, static_cast<int64_t>(0)));
+    const int u_hi = static_cast<int>(min(hi, end) - first);
     if (tid == 0 && u_lo == 0) {
-      const int64_t last = (start + un.total - 1) / slice;
+      const int64_t last = (end - 1) / slice;
       ws.parts[item] = make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
     }
     if (un.groups > un.fixed) {
@@ -545,12 +581,12 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
       __syncthreads();
       if (warp == 0) {
         const int32_t* ids = group_idx + item * p.kg;
-        const int first = un.b_base / p.Ng;
+        const int window = un.b_base / p.Ng;
         int before = -1;
         bool bad = false;
         for (int i0 = 0; i0 < p.kg; i0 += 32) {
           const int id = i0 + lane < p.kg ? ids[i0 + lane] : -1;
-          const bool candidate = id >= 0 && id / p.Ng >= p.sink && id / p.Ng < first;
+          const bool candidate = id >= 0 && id / p.Ng >= p.sink && id / p.Ng < window;
           int m = candidate ? id : -1;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -573,106 +609,107 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
     const int32_t* table = qc.table + item * qc.max_groups;
     const int g_hi = min(u_hi, un.groups);  // groups of the slice: [u_lo, g_hi)
 
-    // table entries of the warp's tile at unit u
-    auto load_slots = [&](int u, int (&slot)[kTile], int (&entry)[kTile]) {
+    // table entries of the warp's tile at unit u; -1: no unit, or no slot, -2: id not kept
+    auto load_slots = [&](int u, int (&slot)[kTile]) {
 #pragma unroll
       for (int j = 0; j < kTile; ++j) {
-        entry[j] = u + j < g_hi ? un.entry(u + j, s_routed) : -1;
         slot[j] = -1;
-        if (entry[j] >= 0) {
-          slot[j] = table[entry[j]];
-          if (slot[j] < 0 || slot[j] >= qc.n_slots) {
+        if (u + j < g_hi) {
+          const int e = un.entry(u + j, s_routed);
+          slot[j] = e >= 0 ? table[e] : -2;
+          if (e >= 0 && (slot[j] < 0 || slot[j] >= qc.n_slots)) {
             if (lane == 0) flag_error(err, kErrPage);
             slot[j] = -1;
           }
         }
       }
     };
-    Raw<D> raw;
-    auto load_k = [&]() {
+    // starts the copies of a tile into a stage
+    auto issue = [&](int stage, const int (&slot)[kTile]) {
 #pragma unroll
       for (int j = 0; j < kTile; ++j) {
-        if (raw.slot[j] >= 0) {
-          const uint8_t* base = qc.k + static_cast<int64_t>(raw.slot[j]) * (kQuantGroup * D) + g * D + c * 16;
+        const bool valid = slot[j] >= 0;
+        const int64_t at = static_cast<int64_t>(valid ? slot[j] : 0) * (kQuantGroup * D);
+        const uint32_t dst = ring_at + (stage * kTile + j) * kUnitBytes;
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) load_stream(base + r * 8 * D + i * 64, raw.k[j][r][i]);
-          raw.ks[j] = qc.k_scale[raw.slot[j]];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-              raw.k[j][r][i][0] = raw.k[j][r][i][1] = raw.k[j][r][i][2] = raw.k[j][r][i][3] = 0u;
-          raw.ks[j] = 0.f;
+        for (int i = 0; i < D / 32; ++i) {  // 512 bytes of K and of V per step
+          const int piece = i * 32 + lane, row = piece / (D / 16), col = piece % (D / 16);
+          const uint32_t to = dst + Tile<D>::piece(row, col);
+          copy16(to, qc.k + at + piece * 16, valid);
+          copy16(to + kQuantGroup * D, qc.v + at + piece * 16, valid);
+        }
+        if (lane < 2) {
+          copy4(scale_at + ((stage * kTile + j) * 2 + lane) * 4, (lane ? qc.v_scale : qc.k_scale) + (valid ? slot[j] : 0), valid);
+          if (lane == 0) s_state[warp][stage][j] = valid ? 1 : slot[j] + 1;
         }
       }
-    };
-    auto load_v = [&]() {
-#pragma unroll
-      for (int j = 0; j < kTile; ++j) {
-        if (raw.slot[j] >= 0) {
-          const uint8_t* base = qc.v + static_cast<int64_t>(raw.slot[j]) * (kQuantGroup * D) + 2 * c * D + g * (D / 8);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) load_stream(base + ((r & 1) + 8 * (r >> 1)) * D, raw.v[j][r]);
-          raw.vs[j] = qc.v_scale[raw.slot[j]];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw.v[j][r][i] = 0u;
-          raw.vs[j] = 0.f;
-        }
-      }
+      copy_commit();
     };
 
     int u = u_lo + warp * kTile;
     constexpr int kStep = kWarps * kTile;
-    int slot_next[kTile], entry_next[kTile];
-    load_slots(u, raw.slot, raw.entry);
-    load_slots(u + kStep, slot_next, entry_next);
-    load_k();
-    load_v();
+    int slot[kStages][kTile], slot_next[kTile];
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) load_slots(u + k * kStep, slot[k]);
+    load_slots(u + kStages * kStep, slot_next);
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) issue(k, slot[k]);
     w.load_q(q, p, b, h);
     w.clear();
-    for (; u < g_hi; u += kStep) {
+    if (u_hi > un.groups && warp == kWarps - 1) {
+      const int64_t at = item * kQuantGroup * D;
+      w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
+             stride, un.groups, p.G);
+    }
+    for (int stage = 0; u < g_hi; u += kStep, stage = stage + 1 == kStages ? 0 : stage + 1) {
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t tile = ring_at + stage * kTile * kUnitBytes;
       float x[kTile][NT][4], mant[kTile], ex[kTile];
       int at[kTile];
       bool kept[kTile];
 #pragma unroll
       for (int j = 0; j < kTile; ++j) {
+        const uint32_t kt = tile + j * kUnitBytes;
+        uint32_t k[2][D / 64][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) load_shared(kt + Tile<D>::piece(Tile<D>::token(g + 8 * r), i * 4 + c), k[r][i]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
           uint32_t a0, a1, a2, a3;
-          widen4<FORMAT>(raw.k[j][0][ks >> 2][ks & 3], a0, a2);
-          widen4<FORMAT>(raw.k[j][1][ks >> 2][ks & 3], a1, a3);
+          widen4<FORMAT>(k[0][ks >> 2][ks & 3], a0, a2);
+          widen4<FORMAT>(k[1][ks >> 2][ks & 3], a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma(x[j][nt], a0, a1, a2, a3, w.qh[nt][ks][0], w.qh[nt][ks][1]);
             if constexpr (W::kSplitQ) mma(x[j][nt], a0, a1, a2, a3, w.ql[nt][ks][0], w.ql[nt][ks][1]);
           }
         }
+        const float k_scale = s_scale[warp][stage][j][0];
+        const int state = s_state[warp][stage][j];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[j][nt][i] = raw.slot[j] >= 0 ? x[j][nt][i] * (w.f[nt][i & 1] * raw.ks[j]) : -CUDART_INF_F;
-        split_scale(raw.vs[j], mant[j], ex[j]);
+            x[j][nt][i] = state > 0 ? x[j][nt][i] * (w.f[nt][i & 1] * k_scale) : -CUDART_INF_F;
+        split_scale(s_scale[warp][stage][j][1], mant[j], ex[j]);
         at[j] = u + j < g_hi ? u + j : -1;
-        kept[j] = raw.entry[j] >= 0;
+        kept[j] = state >= 0;
       }
-#pragma unroll
-      for (int j = 0; j < kTile; ++j) {
-        raw.slot[j] = slot_next[j];
-        raw.entry[j] = entry_next[j];
-      }
-      load_k();
-      load_slots(u + 2 * kStep, slot_next, entry_next);
       uint32_t pb[kTile][NT][2][2];
       w.template softmax<kTile>(x, mant, ex, pb, group, stride, at, kept, p.G);
+      uint32_t v[kTile][4][D / 32];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; D / 8 bytes at g D / 8
+#pragma unroll
+      for (int j = 0; j < kTile; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = Tile<D>::token(2 * c + (r & 1) + 8 * (r >> 1));
+          load_shared(tile + j * kUnitBytes + kQuantGroup * D + Tile<D>::piece(row, g * D / 128) + (D == 64 ? (g & 1) * 8 : 0), v[j][r]);
+        }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         uint32_t a[kTile][2][4];  // the two 16-row tiles of these four bytes
@@ -680,8 +717,8 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
         for (int j = 0; j < kTile; ++j)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint32_t lo16 = __byte_perm(raw.v[j][2 * r][i], raw.v[j][2 * r + 1][i], 0x5140);
-            const uint32_t hi16 = __byte_perm(raw.v[j][2 * r][i], raw.v[j][2 * r + 1][i], 0x7362);
+            const uint32_t lo16 = __byte_perm(v[j][2 * r][i], v[j][2 * r + 1][i], 0x5140);
+            const uint32_t hi16 = __byte_perm(v[j][2 * r][i], v[j][2 * r + 1][i], 0x7362);
             widen4<FORMAT>(lo16, a[j][0][2 * r], a[j][0][2 * r + 1]);
             widen4<FORMAT>(hi16, a[j][1][2 * r], a[j][1][2 * r + 1]);
           }
@@ -700,14 +737,12 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
             for (int e = 0; e < 4; ++e) w.o[2 * i + half][nt][e] += s[e];
           }
       }
-      load_v();
+      __syncwarp();  // every lane has read the stage
+      issue(stage, slot_next);
+      load_slots(u + (kStages + 1) * kStep, slot_next);
     }
-
-    if (u_hi > un.groups && warp == kWarps - 1) {
-      const int64_t at = item * kQuantGroup * D;
-      w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
-             stride, un.groups, p.G);
-    }
+    copy_wait<0>();
+    __syncwarp();
 
     // merge the warps
 #pragma unroll
@@ -725,7 +760,7 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
             y1 += __shfl_xor_sync(0xffffffffu, y1, 2);
           }
           if (GM != 4 || c < 2)
-            *reinterpret_cast<float2*>(&s_sum[warp][head][mt * 16 + g * 2]) = make_float2(y0, y1);
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(ring) + head * kRow + mt * 16 + g * 2) = make_float2(y0, y1);
         }
         if (g == 0 && (GM != 4 || c < 2)) {
           s_stat[warp][head][0] = w.ref_w[nt][e];
@@ -742,7 +777,8 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
       for (int k = 1; k < kWarps; ++k) ref = fmaxf(ref, s_stat[k][head][0]);
       float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) sum += s_sum[k][head][d] * ex2(s_stat[k][head][0] - ref);
+      for (int k = 0; k < kWarps; ++k)
+        sum += reinterpret_cast<const float*>(s_dyn + k * kRing)[head * kRow + d] * ex2(s_stat[k][head][0] - ref);
       ws.sum[(part * p.G + head) * D + d] = sum;
     }
     if (tid < p.G) {
@@ -757,8 +793,7 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
       *reinterpret_cast<float4*>(ws.stat + (part * 16 + tid) * 4) = make_float4(rw, rs, l, 0.f);
     }
     __syncthreads();
-    start += un.total;
-    next = start;
+    next = start = end;
   }
   pdl_trigger();
 }
@@ -908,11 +943,13 @@ cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
   int64_t most = qc.max_groups;
   if (group_idx) most = std::min(most, static_cast<int64_t>(p.sink + p.local + 1) * p.Ng) + p.kg + 1;
-  const int64_t slices = (items * most + kMinSlice - 1) / kMinSlice;
+  const int64_t slices = (items * (most + kItemCost) + kMinSlice - 1) / kMinSlice;
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(GM);
   const unsigned grid = static_cast<unsigned>(slices < resident ? slices : resident);
-  return launch_pdl(quant_attend_kernel<T, D, FORMAT, GM>, dim3(grid), dim3(kThreads),
-                    group_idx ? p.kg * sizeof(int) : 0, s, 1, p, qc, static_cast<const T*>(q), pos,
+  const size_t smem = kWarps * kStages * kTile * Tile<D>::kUnitBytes + (group_idx ? p.kg * sizeof(int) : 0);
+  cudaError_t e = ensure_smem<quant_attend_kernel<T, D, FORMAT, GM>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(quant_attend_kernel<T, D, FORMAT, GM>, dim3(grid), dim3(kThreads), smem, s, 1, p, qc, static_cast<const T*>(q), pos,
                     group_idx, ws, err);
 }
 
