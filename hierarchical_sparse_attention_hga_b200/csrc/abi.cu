@@ -567,8 +567,9 @@ static hga_status quant_params(const hga_config* cfg, const hga_quant_cache* cac
     return fail(HGA_ERR_INVALID_ARG, "format %d", cache->format);
   if (cache->max_groups <= 0 || cache->n_slots <= 0)
     return fail(HGA_ERR_INVALID_ARG, "max_groups and n_slots must be positive");
-  if (cache->max_groups > kQuantMaxGroups || cache->n_slots > 0x7fffffffLL)
-    return fail(HGA_ERR_UNSUPPORTED, "max_groups above %d or n_slots above 2^31 - 1", kQuantMaxGroups);
+  if (cache->max_groups > kQuantMaxGroups || cache->n_slots > kQuantMaxSlots)
+    return fail(HGA_ERR_UNSUPPORTED, "max_groups above %d or n_slots above %lld", kQuantMaxGroups,
+                static_cast<long long>(kQuantMaxSlots));
   p->n_alloc = static_cast<int64_t>(cache->max_groups) * kQuantGroup;
   p->n_chunks = static_cast<int>(p->n_alloc / p->C);
   *out = QuantCache{static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), cache->k_scale,

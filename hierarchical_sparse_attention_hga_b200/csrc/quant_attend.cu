@@ -8,8 +8,8 @@
 // tokens and the G query heads of the KV head, is added to an accumulator.
 //
 // Bound by HBM: 2 D bytes a token are read once, for 4 G D operations.  Each warp
-// streams groups through a ring of its own in shared memory (16-byte
-// asynchronous copies, each 512 contiguous bytes a warp), reads the codes back in
+// streams groups through a ring of its own in shared memory (one TMA box for a
+// group's K, one for its V), reads the codes back in
 // the very bytes that the matrix instruction's operand layout wants from each
 // lane, widens them in registers to f16 (exact for both formats) and multiplies
 // on mma.sync m16n8k16 with the TOKENS as the 16 rows and the query heads as the
@@ -30,16 +30,20 @@
 // nearest): the matrix unit's own accumulation is never longer than a tile.
 //
 // Work.  A fixed grid; the units (groups, and one for a tail) of all items form
-// one list, of which each CTA takes an equal slice, whatever the sequences'
+// one list, of which each warp takes an equal slice, whatever the sequences'
 // lengths.  Every item stands there with kItemCost more units than it has, for
-// what it costs beside its bytes.  A CTA leaves one partial (sum, reference, denominator) per item it
-// touches, at slot CTA + item (distinct, since one of the two grows from each
-// partial to the next); a second kernel merges them, in a fixed order.
+// what it costs beside its bytes.  A warp leaves one partial (sum, references,
+// denominator) per item it touches, at slot warp + item (distinct, since one of
+// the two grows from each partial to the next); a second kernel merges them, in
+// a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 #include "quant_cache.cuh"
+#include "tmap.h"
 
 namespace hga {
 namespace {
@@ -48,10 +52,12 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 2;             // units a warp works on at a time
 constexpr int kStages = 2;           // tiles in a warp's ring
-constexpr int kItemCost = 16;        // an item's fixed work, in units (see the slices)
-constexpr int kMinSlice = kWarps * kTile;
+static_assert(32 % kTile == 0, "a tile's slots come from one block of 32");
+constexpr int kItemCost = 4;         // an item's fixed work, in units (see the slices)
+constexpr int kMinSlice = 2;         // units a warp takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kWaitLimit = 1u << 26;  // bounded mbarrier polls (and 50 ms)
 constexpr float kNoRef = -1e30f;     // reference before the first score
 constexpr float kHeadroom = 2.f;     // a raised reference exceeds the maximum by 2 to 3
 constexpr float kWeightExp = 14.f;   // weights are at most 2 * 2^(14 - 2) in f16
@@ -79,10 +85,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// 16 bytes from global to shared memory; zeros when !valid (nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
+// 4 bytes from global to shared memory; zero when !valid (nothing is read).
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
@@ -97,9 +100,10 @@ __device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&r)[2]) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
 
-// One unit's codes in shared memory: K rows, then V rows, D bytes each, with the
-// 16-byte pieces of row r permuted by an XOR.  Row n of the matrix products is
-// token token(n), so that
+// One unit's codes in shared memory: K rows, then V rows, D bytes each, the
+// 16-byte pieces of a row permuted as the copy's swizzle does it (128-byte rows:
+// by the row's low three bits; 64-byte rows: by bits 1 and 2).  Row n of the
+// matrix products is token token(n), so that
 //  - K: the two rows that eight lanes read (n = 2m, 2m + 1; 64 bytes of each) lie
 //    in different halves of the banks,
 //  - V: the four rows (n = 2c, or 2c + 1) and the neighbouring pieces that a
@@ -108,11 +112,13 @@ template <int D>
 struct Tile {
   static constexpr int kUnitBytes = 2 * kQuantGroup * D;
   static __device__ __forceinline__ int token(int n) {
-    const int c = (n & 7) >> 1, even = D == 128 ? 2 * c : c;
-    return (n & 8) | ((n & 1) ? even ^ 5 : even);
+    const int c = (n & 7) >> 1;
+    if (D == 128) return (n & 8) | ((n & 1) ? (2 * c) ^ 5 : 2 * c);
+    const int even = (c & 1) | ((c & 2) << 1);
+    return (n & 8) | ((n & 1) ? even ^ 3 : even);
   }
   static __device__ __forceinline__ int piece(int row, int i) {
-    return row * D + ((i ^ (D == 128 ? row & 7 : row & 2)) << 4);
+    return row * D + ((i ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
   }
 };
 
@@ -199,9 +205,9 @@ __device__ __forceinline__ Units units_of(const LayerParams& p, const QuantItem&
 
 // Scratch of one call.
 struct Workspace {
-  int2* parts;     // [items]: first CTA of the item, number of CTAs
-  float* stat;     // [ctas + items][16][4]: weight reference, score reference, denominator
-  float* sum;      // [ctas + items][G][D], dimensions in the kernel's order
+  int2* parts;     // [items]: first warp of the item, number of warps
+  float* stat;     // [warps + items][16][4]: weight reference, score reference, denominator
+  float* sum;      // [warps + items][G][D], dimensions in the kernel's order
   float2* group;   // [items][G][max_groups + kg]: each unit's sum (-1: a routed id that is not
                    // kept) and its reference, in the virtual list's order (weights only)
 };
@@ -367,114 +373,124 @@ struct Warp {
       }
   }
 
-  // Tail rows (rest of them valid) as one unit.
+  // Tail rows (rest of them valid) as one unit.  All loads come first.
   __device__ void tail(const T* kt, const T* vt, int rest, float2* group, int stride, int unit, int G) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float x[1][NT][4];
-    int e_k, e_v;
-    {
-      float k[2][NK][4];
-      uint32_t top = 0;
+    using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
+    Row kr[2][NK], vr[4][D / 32];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int ks = 0; ks < NK; ++ks) {
-          const int row = g + 8 * r;
-          if (row < rest)
-            load_row(kt + row * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, k[r][ks]);
-          else
-            k[r][ks][0] = k[r][ks][1] = k[r][ks][2] = k[r][ks][3] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = max(top, finite_bits(k[r][ks][i]));
-        }
-      e_k = scale_exponent(__reduce_max_sync(0xffffffffu, top));
-      const float up = exp2i(14 - e_k);
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
-        uint32_t a[4], b[4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) k[r][ks][i] *= up;
-          a[r] = pack_half2(k[r][ks][0], k[r][ks][1]);
-          a[r + 2] = pack_half2(k[r][ks][2], k[r][ks][3]);
-          b[r] = pack_rest(k[r][ks][0], k[r][ks][1], a[r]);
-          b[r + 2] = pack_rest(k[r][ks][2], k[r][ks][3], a[r + 2]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma(s[nt], a[0], a[1], a[2], a[3], qh[nt][ks][0], qh[nt][ks][1]);
-          if constexpr (kSplitQ) {
-            mma(s[nt], a[0], a[1], a[2], a[3], ql[nt][ks][0], ql[nt][ks][1]);
-            mma(s[nt], b[0], b[1], b[2], b[3], qh[nt][ks][0], qh[nt][ks][1]);
-          }
-        }
+        kr[r][ks] = Row{};
+        if (g + 8 * r < rest)
+          kr[r][ks] = *reinterpret_cast<const Row*>(kt + (g + 8 * r) * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4);
       }
-      const float down = exp2i(e_k - 14);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float fs = f[nt][i & 1] * down;
-          x[0][nt][i] = g + 8 * (i >> 1) < rest ? s[nt][i] * fs : -CUDART_INF_F;
-        }
-    }
     // V: rows 2c, 2c + 1, 2c + 8, 2c + 9, this lane's D / 8 dimensions
-    float v[4][D / 8];
-    uint32_t top = 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 2 * c + (r & 1) + 8 * (r >> 1);
 #pragma unroll
-      for (int j = 0; j < D / 8; j += 4) {
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (row < rest) load_row(vt + row * D + g * (D / 8) + j, y);
+      for (int j = 0; j < D / 32; ++j) {
+        vr[r][j] = Row{};
+        if (row < rest) vr[r][j] = *reinterpret_cast<const Row*>(vt + row * D + g * (D / 8) + 4 * j);
+      }
+    }
+    uint32_t top_k = 0, top_v = 0;
+    float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[r][j + i] = y[i];
-          top = max(top, finite_bits(y[i]));
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        unpack(kr[r][ks], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top_k = max(top_k, finite_bits(y[i]));
+      }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        unpack(vr[r][j], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top_v = max(top_v, finite_bits(y[i]));
+      }
+    const int e_k = scale_exponent(__reduce_max_sync(0xffffffffu, top_k));
+    const int e_v = scale_exponent(__reduce_max_sync(0xffffffffu, top_v));
+    const float up_k = exp2i(14 - e_k), down_k = exp2i(e_k - 14), up_v = exp2i(14 - e_v);
+    float x[1][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) x[0][nt][0] = x[0][nt][1] = x[0][nt][2] = x[0][nt][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        unpack(kr[r][ks], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= up_k;
+        a[r] = pack_half2(y[0], y[1]);
+        a[r + 2] = pack_half2(y[2], y[3]);
+        if constexpr (kSplitQ) {
+          b[r] = pack_rest(y[0], y[1], a[r]);
+          b[r + 2] = pack_rest(y[2], y[3], a[r + 2]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma(x[0][nt], a[0], a[1], a[2], a[3], qh[nt][ks][0], qh[nt][ks][1]);
+        if constexpr (kSplitQ) {
+          mma(x[0][nt], a[0], a[1], a[2], a[3], ql[nt][ks][0], ql[nt][ks][1]);
+          mma(x[0][nt], b[0], b[1], b[2], b[3], qh[nt][ks][0], qh[nt][ks][1]);
         }
       }
     }
-    e_v = scale_exponent(__reduce_max_sync(0xffffffffu, top));
-    const float up = exp2i(14 - e_v);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[0][nt][i] = g + 8 * (i >> 1) < rest ? x[0][nt][i] * (f[nt][i & 1] * down_k) : -CUDART_INF_F;
     const float mant[1] = {1.f}, ex[1] = {static_cast<float>(e_v - 14)};
     const int at[1] = {unit};
     const bool kept[1] = {true};
     uint32_t pb[1][NT][2][2];
     softmax<1>(x, mant, ex, pb, group, stride, at, kept, G);
 #pragma unroll
-    for (int mt = 0; mt < NK; ++mt) {
-      uint32_t a[4], b[4];
+    for (int j = 0; j < D / 32; ++j) {
+      float v[4][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < 4; ++r) {
+        unpack(vr[r][j], v[r]);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const float y0 = v[2 * r][2 * mt + d] * up, y1 = v[2 * r + 1][2 * mt + d] * up;
-          a[2 * r + d] = pack_half2(y0, y1);
-          b[2 * r + d] = pack_rest(y0, y1, a[2 * r + d]);
+        for (int i = 0; i < 4; ++i) v[r][i] *= up_v;
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const float y0 = v[2 * r][2 * half + d], y1 = v[2 * r + 1][2 * half + d];
+            a[2 * r + d] = pack_half2(y0, y1);
+            if constexpr (kSplitQ) b[2 * r + d] = pack_rest(y0, y1, a[2 * r + d]);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          mma(s, a[0], a[1], a[2], a[3], pb[0][nt][0][0], pb[0][nt][0][1]);
+          if constexpr (GM != 4) mma(s, a[0], a[1], a[2], a[3], pb[0][nt][1][0], pb[0][nt][1][1]);
+          if constexpr (kSplitQ) mma(s, b[0], b[1], b[2], b[3], pb[0][nt][0][0], pb[0][nt][0][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[2 * j + half][nt][i] += s[i];
         }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        mma(s, a[0], a[1], a[2], a[3], pb[0][nt][0][0], pb[0][nt][0][1]);
-        if constexpr (GM != 4) mma(s, a[0], a[1], a[2], a[3], pb[0][nt][1][0], pb[0][nt][1][1]);
-        if constexpr (kSplitQ) mma(s, b[0], b[1], b[2], b[3], pb[0][nt][0][0], pb[0][nt][0][1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][nt][i] += s[i];
       }
     }
   }
 
-  static __device__ __forceinline__ void load_row(const float* p, float (&y)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
+  static __device__ __forceinline__ void unpack(const float4& v, float (&y)[4]) {
     y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
   }
-  static __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&y)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
+  static __device__ __forceinline__ void unpack(const uint2& v, float (&y)[4]) {
     y[0] = __uint_as_float(v.x << 16); y[1] = __uint_as_float(v.x & 0xffff0000u);
     y[2] = __uint_as_float(v.y << 16); y[3] = __uint_as_float(v.y & 0xffff0000u);
   }
@@ -482,188 +498,215 @@ struct Warp {
 
 template <typename T, int D, int FORMAT, int GM>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(GM))
-quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
+quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    LayerParams p, QuantCache qc, const T* __restrict__ q,
                     const int64_t* __restrict__ pos, const int32_t* __restrict__ group_idx,
                     Workspace ws, unsigned* err) {
   using W = Warp<T, D, FORMAT, GM>;
   constexpr int NT = W::NT, NK = W::NK;
-  constexpr int kRow = D + 8;  // padded row of the merge buffer
   constexpr int kUnitBytes = Tile<D>::kUnitBytes;
   constexpr int kRing = kStages * kTile * kUnitBytes;
-  static_assert(GM * kRow * 4 <= kRing, "a warp's partial sum reuses its ring");
-  extern __shared__ __align__(16) uint8_t s_dyn[];  // [kWarps][kRing], then [kg] routed ids
-  int* s_routed = reinterpret_cast<int*>(s_dyn + kWarps * kRing);
+  extern __shared__ uint8_t s_dyn[];                    // [kWarps][kRing], then [kWarps][kg] routed ids
+  uint8_t* s_rings = s_dyn + (1024 - ptx::smem_u32(s_dyn) % 1024) % 1024;
+  __shared__ uint64_t s_full[kWarps][kStages];
   __shared__ float s_scale[kWarps][kStages][kTile][2];  // k_scale, v_scale
   __shared__ int s_state[kWarps][kStages][kTile];       // 1: in the ring, 0: no tokens, -1: id not kept
-  __shared__ float s_stat[kWarps][GM][3];
-  __shared__ int64_t s_part[kThreads];
-  __shared__ int64_t s_start;
-  __shared__ int s_item;
+  __shared__ int64_t s_before[kThreads];                // list length before each thread's items
+  __shared__ int64_t s_all;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = s_dyn + warp * kRing;
-  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  const uint32_t scale_at = static_cast<uint32_t>(__cvta_generic_to_shared(&s_scale[warp][0][0][0]));
-  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
+  uint8_t* ring = s_rings + warp * kRing;
+  const uint32_t ring_at = ptx::smem_u32(ring), scale_at = ptx::smem_u32(&s_scale[warp][0][0][0]);
+  int* routed = reinterpret_cast<int*>(s_rings + kWarps * kRing) + warp * p.kg;
+  const int items = p.B * p.Hkv;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) ptx::mbar_init(&s_full[warp][k], 1);
+    ptx::fence_barrier_init();
+  }
   pdl_wait();
 
+  auto worker = [&]() { return static_cast<int64_t>(blockIdx.x) * kWarps + warp; };
+  auto slice_length = [&](int64_t all) {
+    const int64_t slices = static_cast<int64_t>(gridDim.x) * kWarps;
+    return max(static_cast<int64_t>(kMinSlice), (all + slices - 1) / slices);
+  };
   // an item's length in the list of all items' units, its fixed work in front
-  auto item_length = [&](int64_t i, unsigned* e) {
+  auto item_length = [&](int i, unsigned* e) {
     const int64_t pb = pos[i / p.Hkv];
     const int n = units_of(p, quant_item(qc, pb, i, e), pb, group_idx != nullptr).total;
     return n ? n + kItemCost : 0;
   };
-  // where this CTA's slice [lo, hi) of the list begins
-  const int64_t per = (items + kThreads - 1) / kThreads;
-  const int64_t i_lo = min(items, tid * per), i_hi = min(items, i_lo + per);
-  int64_t mine = 0;
-  for (int64_t i = i_lo; i < i_hi; ++i) mine += item_length(i, blockIdx.x == 0 ? err : nullptr);
-  s_part[tid] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t v[kThreads / 32], sum = 0;
+  // where this warp's slice [lo, hi) of the list begins
+  const int per = (items + kThreads - 1) / kThreads;
+  {
+    int64_t mine = 0;
+    for (int i = min(items, tid * per); i < min(items, (tid + 1) * per); ++i)
+      mine += item_length(i, blockIdx.x == 0 ? err : nullptr);
+    s_before[tid] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t v[kWarps], sum = 0;
 #pragma unroll
-    for (int j = 0; j < kThreads / 32; ++j) {
-      v[j] = s_part[lane * (kThreads / 32) + j];
-      sum += v[j];
-    }
-    int64_t x = sum;
+      for (int j = 0; j < kWarps; ++j) {
+        v[j] = s_before[lane * kWarps + j];
+        sum += v[j];
+      }
+      int64_t x = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    int64_t run = x - sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      int64_t run = x - sum;
 #pragma unroll
-    for (int j = 0; j < kThreads / 32; ++j) {
-      s_part[lane * (kThreads / 32) + j] = run;
-      run += v[j];
+      for (int j = 0; j < kWarps; ++j) {
+        s_before[lane * kWarps + j] = run;
+        run += v[j];
+      }
+      if (lane == 31) s_all = x;
     }
-    if (lane == 31) s_start = x;  // the whole list
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t all = s_start;
-  int64_t slice = (all + gridDim.x - 1) / gridDim.x;
-  slice = max(static_cast<int64_t>(kMinSlice), (slice + kTile - 1) / kTile * kTile);
-  const int64_t lo = slice * blockIdx.x, hi = min(all, lo + slice);
-  if (lo >= hi) return;
-  __syncthreads();
-  if (s_part[tid] <= lo && lo < s_part[tid] + mine) {
-    int64_t at = s_part[tid];
-    int64_t i = i_lo;
-    for (;; ++i) {
-      const int n = item_length(i, nullptr);
-      if (lo < at + n) break;
-      at += n;
+  int item;
+  int skip;   // of the item's length, where the slice enters it
+  int left;   // of the slice (at most the longest item's length, or a 1000th of the list)
+  {
+    const int64_t all = s_all, slice = slice_length(all);
+    const int64_t lo = slice * worker();
+    if (lo >= all) return;
+    left = static_cast<int>(min(slice, all - lo));
+    int owner = -1;  // the last thread whose items begin at or before lo
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) owner += __popc(__ballot_sync(0xffffffffu, s_before[j * 32 + lane] <= lo));
+    int64_t start = s_before[owner];  // where the item begins in the list
+    for (item = owner * per;; item += 32) {
+      const int n = item + lane < items ? item_length(item + lane, nullptr) : 0;
+      int64_t x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned beyond = __ballot_sync(0xffffffffu, start + x > lo);
+      if (beyond) {
+        const int j = __ffs(beyond) - 1;
+        start += __shfl_sync(0xffffffffu, x - n, j);
+        item += j;
+        break;
+      }
+      start += __shfl_sync(0xffffffffu, x, 31);
     }
-    s_item = static_cast<int>(i);
-    s_start = at;
+    skip = static_cast<int>(lo - start);
   }
-  __syncthreads();
-  int64_t item = s_item, start = s_start;
 
   W w;
-  for (int64_t next = lo; next < hi; ++item) {
-    const int b = static_cast<int>(item / p.Hkv), h = static_cast<int>(item % p.Hkv);
+  int stage = 0;       // of the ring, and its phase
+  uint32_t phase = 0;
+  bool alive = true;   // no wait gave up
+  for (; left > 0; ++item) {
+    const int b = item / p.Hkv, h = item % p.Hkv;
     const int64_t pb = pos[b];
     const QuantItem it = quant_item(qc, pb, item, nullptr);
     const Units un = units_of(p, it, pb, group_idx != nullptr);
     if (un.total == 0) continue;
-    const int64_t first = start + kItemCost, end = first + un.total;
-    if (hi <= first) break;  // only the item's fixed part
-    const int u_lo = static_cast<int>(max(next - first, static_cast<int64_t>(0)));
-    const int u_hi = static_cast<int>(min(hi, end) - first);
-    if (tid == 0 && u_lo == 0) {
-      const int64_t last = (end - 1) / slice;
-      ws.parts[item] = make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
+    const int u_lo = max(skip - kItemCost, 0);
+    const int u_hi = min(skip + left - kItemCost, un.total);
+    if (u_hi <= 0) break;  // only the item's fixed part
+    left -= un.total + kItemCost - skip;
+    skip = 0;
+    if (lane == 0 && u_lo == 0) {  // this warp has the item's first unit; its last one is total - u_hi further on
+      const int64_t slice = slice_length(s_all);
+      ws.parts[item] = make_int2(static_cast<int>(worker()), static_cast<int>((max(0, -left) + slice - 1) / slice) + 1);
     }
     if (un.groups > un.fixed) {
       // kept: ids of candidate chunks, larger than all candidate ids before them
-      __syncthreads();
-      if (warp == 0) {
-        const int32_t* ids = group_idx + item * p.kg;
-        const int window = un.b_base / p.Ng;
-        int before = -1;
-        bool bad = false;
-        for (int i0 = 0; i0 < p.kg; i0 += 32) {
-          const int id = i0 + lane < p.kg ? ids[i0 + lane] : -1;
-          const bool candidate = id >= 0 && id / p.Ng >= p.sink && id / p.Ng < window;
-          int m = candidate ? id : -1;
+      const int32_t* ids = group_idx + static_cast<int64_t>(item) * p.kg;
+      const int window = un.b_base / p.Ng;
+      int before = -1;
+      bool bad = false;
+      for (int i0 = 0; i0 < p.kg; i0 += 32) {
+        const int id = i0 + lane < p.kg ? ids[i0 + lane] : -1;
+        const bool candidate = id >= 0 && id / p.Ng >= p.sink && id / p.Ng < window;
+        int m = candidate ? id : -1;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, m, o);
-            if (lane >= o) m = max(m, y);
-          }
-          int prev = __shfl_up_sync(0xffffffffu, m, 1);
-          prev = max(before, lane ? prev : -1);
-          const bool keep = candidate && id > prev;
-          bad |= id >= 0 && !keep;
-          if (i0 + lane < p.kg) s_routed[i0 + lane] = keep ? id : -1;
-          before = max(before, __shfl_sync(0xffffffffu, m, 31));
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, m, o);
+          if (lane >= o) m = max(m, y);
         }
-        if (bad) flag_error(err, kErrGroupIdx);
+        int prev = __shfl_up_sync(0xffffffffu, m, 1);
+        prev = max(before, lane ? prev : -1);
+        const bool keep = candidate && id > prev;
+        bad |= id >= 0 && !keep;
+        if (i0 + lane < p.kg) routed[i0 + lane] = keep ? id : -1;
+        before = max(before, __shfl_sync(0xffffffffu, m, 31));
       }
-      __syncthreads();
+      if (bad) flag_error(err, kErrGroupIdx);
+      __syncwarp();
     }
     const int stride = qc.max_groups + p.kg;
-    float2* group = ws.group ? ws.group + item * p.G * stride : nullptr;
-    const int32_t* table = qc.table + item * qc.max_groups;
+    float2* group = ws.group ? ws.group + static_cast<int64_t>(item) * p.G * stride : nullptr;
+    const int32_t* table = qc.table + static_cast<int64_t>(item) * qc.max_groups;
     const int g_hi = min(u_hi, un.groups);  // groups of the slice: [u_lo, g_hi)
 
-    // table entries of the warp's tile at unit u; -1: no unit, or no slot, -2: id not kept
-    auto load_slots = [&](int u, int (&slot)[kTile]) {
+    // The slots of the slice's units, 32 at a time: lane i has the one of unit
+    // base + i, loaded (unchecked) a block ahead.  -1: no unit, or no slot, -2: id
+    // not kept.
+    auto load_slots = [&](int base) {
+      const int e = base + lane < g_hi ? un.entry(base + lane, routed) : -1;
+      return e >= 0 ? table[e] : -1;
+    };
+    auto checked = [&](int slot, int base) {
+      if (base + lane >= g_hi) return -1;
+      if (un.entry(base + lane, routed) < 0) return -2;
+      if (slot >= 0 && slot < qc.n_slots) return slot;
+      flag_error(err, kErrPage);
+      return -1;
+    };
+    // starts the copies of the slice's next tile, if there is one left
+    int slots = 0, slots_next = load_slots(u_lo), issued = 0;
+    auto issue = [&](int stage) {
+      if (u_lo + issued < g_hi) {
+        if ((issued & 31) == 0) {
+          slots = checked(slots_next, u_lo + issued);
+          slots_next = load_slots(u_lo + issued + 32);
+        }
+        uint8_t* dst = ring + stage * kTile * kUnitBytes;
+        if (lane == 0) ptx::mbar_expect_tx(&s_full[warp][stage], kTile * kUnitBytes);
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) {
-        slot[j] = -1;
-        if (u + j < g_hi) {
-          const int e = un.entry(u + j, s_routed);
-          slot[j] = e >= 0 ? table[e] : -2;
-          if (e >= 0 && (slot[j] < 0 || slot[j] >= qc.n_slots)) {
-            if (lane == 0) flag_error(err, kErrPage);
-            slot[j] = -1;
+        for (int j = 0; j < kTile; ++j) {
+          const int slot = __shfl_sync(0xffffffffu, slots, (issued & 31) + j);
+          const bool valid = slot >= 0;
+          if (lane < 2)
+            copy4(scale_at + ((stage * kTile + j) * 2 + lane) * 4, (lane ? qc.v_scale : qc.k_scale) + (valid ? slot : 0), valid);
+          if (lane == 0) {  // a row before the first reads as zeros
+            const int row = valid ? slot * kQuantGroup : -kQuantGroup;
+            ptx::tma_load_2d(dst + j * kUnitBytes, &map_k, &s_full[warp][stage], 0, row);
+            ptx::tma_load_2d(dst + j * kUnitBytes + kUnitBytes / 2, &map_v, &s_full[warp][stage], 0, row);
+            s_state[warp][stage][j] = valid ? 1 : slot + 1;
           }
         }
-      }
-    };
-    // starts the copies of a tile into a stage
-    auto issue = [&](int stage, const int (&slot)[kTile]) {
-#pragma unroll
-      for (int j = 0; j < kTile; ++j) {
-        const bool valid = slot[j] >= 0;
-        const int64_t at = static_cast<int64_t>(valid ? slot[j] : 0) * (kQuantGroup * D);
-        const uint32_t dst = ring_at + (stage * kTile + j) * kUnitBytes;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {  // 512 bytes of K and of V per step
-          const int piece = i * 32 + lane, row = piece / (D / 16), col = piece % (D / 16);
-          const uint32_t to = dst + Tile<D>::piece(row, col);
-          copy16(to, qc.k + at + piece * 16, valid);
-          copy16(to + kQuantGroup * D, qc.v + at + piece * 16, valid);
-        }
-        if (lane < 2) {
-          copy4(scale_at + ((stage * kTile + j) * 2 + lane) * 4, (lane ? qc.v_scale : qc.k_scale) + (valid ? slot[j] : 0), valid);
-          if (lane == 0) s_state[warp][stage][j] = valid ? 1 : slot[j] + 1;
-        }
+        issued += kTile;
       }
       copy_commit();
     };
 
-    int u = u_lo + warp * kTile;
-    constexpr int kStep = kWarps * kTile;
-    int slot[kStages][kTile], slot_next[kTile];
+    int u = u_lo;
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) load_slots(u + k * kStep, slot[k]);
-    load_slots(u + kStages * kStep, slot_next);
-#pragma unroll
-    for (int k = 0; k < kStages; ++k) issue(k, slot[k]);
+    for (int k = 0; k < kStages; ++k) issue((stage + k) % kStages);
     w.load_q(q, p, b, h);
     w.clear();
-    if (u_hi > un.groups && warp == kWarps - 1) {
-      const int64_t at = item * kQuantGroup * D;
+    if (u_hi > un.groups) {
+      const int64_t at = static_cast<int64_t>(item) * kQuantGroup * D;
       w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
              stride, un.groups, p.G);
     }
-    for (int stage = 0; u < g_hi; u += kStep, stage = stage + 1 == kStages ? 0 : stage + 1) {
+    for (; u < g_hi; u += kTile) {
       copy_wait<kStages - 1>();
-      __syncwarp();
+      // after a wait gave up, the others are short; every copy is still waited for
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_ns(&s_full[warp][stage], phase, kWaitLimit, alive ? 50000000ull : 1000000ull))) {
+        alive = false;
+        flag_error(err, kErrTimeout);
+      }
       const uint32_t tile = ring_at + stage * kTile * kUnitBytes;
       float x[kTile][NT][4], mant[kTile], ex[kTile];
       int at[kTile];
@@ -738,13 +781,16 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
           }
       }
       __syncwarp();  // every lane has read the stage
-      issue(stage, slot_next);
-      load_slots(u + (kStages + 1) * kStep, slot_next);
+      issue(stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    copy_wait<0>();
-    __syncwarp();
 
-    // merge the warps
+    // this slice's partial of the item (empty if a wait gave up)
+    if (!alive) w.clear();
+    const int64_t part = worker() + item;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -752,64 +798,38 @@ quant_attend_kernel(LayerParams p, QuantCache qc, const T* __restrict__ q,
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) w.l[nt][e] += __shfl_xor_sync(0xffffffffu, w.l[nt][e], k);
         const int head = nt * 8 + 2 * c + e;
+        const bool mine = head < p.G && (GM != 4 || c < 2);
 #pragma unroll
         for (int mt = 0; mt < NK; ++mt) {
           float y0 = w.o[mt][nt][e], y1 = w.o[mt][nt][e + 2];
-          if constexpr (GM == 4) {
+          if constexpr (GM == 4) {  // the low halves' columns
             y0 += __shfl_xor_sync(0xffffffffu, y0, 2);
             y1 += __shfl_xor_sync(0xffffffffu, y1, 2);
           }
-          if (GM != 4 || c < 2)
-            *reinterpret_cast<float2*>(reinterpret_cast<float*>(ring) + head * kRow + mt * 16 + g * 2) = make_float2(y0, y1);
+          if (mine) *reinterpret_cast<float2*>(ws.sum + (part * p.G + head) * D + mt * 16 + g * 2) = make_float2(y0, y1);
         }
-        if (g == 0 && (GM != 4 || c < 2)) {
-          s_stat[warp][head][0] = w.ref_w[nt][e];
-          s_stat[warp][head][1] = w.ref_s[nt][e];
-          s_stat[warp][head][2] = w.l[nt][e];
-        }
+        if (mine && g == 0)
+          *reinterpret_cast<float4*>(ws.stat + (part * 16 + head) * 4) =
+              make_float4(w.ref_w[nt][e], w.ref_s[nt][e], w.l[nt][e], 0.f);
       }
-    __syncthreads();
-    const int64_t part = blockIdx.x + item;
-    for (int i = tid; i < p.G * D; i += kThreads) {
-      const int head = i / D, d = i % D;
-      float ref = s_stat[0][head][0];
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k) ref = fmaxf(ref, s_stat[k][head][0]);
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        sum += reinterpret_cast<const float*>(s_dyn + k * kRing)[head * kRow + d] * ex2(s_stat[k][head][0] - ref);
-      ws.sum[(part * p.G + head) * D + d] = sum;
-    }
-    if (tid < p.G) {
-      float rw = kNoRef, rs = kNoRef, l = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        rw = fmaxf(rw, s_stat[k][tid][0]);
-        rs = fmaxf(rs, s_stat[k][tid][1]);
-      }
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) l += s_stat[k][tid][2] * ex2(s_stat[k][tid][1] - rs);
-      *reinterpret_cast<float4*>(ws.stat + (part * 16 + tid) * 4) = make_float4(rw, rs, l, 0.f);
-    }
-    __syncthreads();
-    next = start = end;
   }
   pdl_trigger();
 }
 
-// Merges an item's partials.  Block y < G: query head y's output and LSE; block
-// y >= G: the weights of 1024 table entries.
-constexpr int kMergeThreads = 256;
+// Merges an item's partials.  The first blocks along y: outputs and LSE of
+// kMergeWarps / SPLIT query heads each, SPLIT warps sharing a head's partials;
+// the blocks behind them: the weights of 1024 table entries each.
 constexpr int kMergeEntries = 1024;
-template <int D, typename TO>
-__global__ void __launch_bounds__(kMergeThreads)
+constexpr int merge_warps(int split) { return split > 1 ? split : 8; }
+template <int D, typename TO, int SPLIT>
+__global__ void __launch_bounds__(merge_warps(SPLIT) * 32)
 quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos, Workspace ws,
                    const int32_t* __restrict__ group_idx, const float* weight_in,
                    float* weight_out, TO* __restrict__ out,
                    float* __restrict__ lse) {
-  constexpr int kMergeWarps = kMergeThreads / 32;
-  __shared__ float s_sum[kMergeWarps][D];
+  constexpr int kMergeWarps = merge_warps(SPLIT), kMergeThreads = kMergeWarps * 32;
+  constexpr int kHeads = kMergeWarps / SPLIT;
+  __shared__ float s_sum[SPLIT > 1 ? kMergeWarps : 1][D];
   __shared__ float s_l[kMergeWarps];
   __shared__ float s_ref[16][2];
   __shared__ float s_add[kMergeEntries];
@@ -822,46 +842,57 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
   const int2 parts = units ? ws.parts[item] : make_int2(0, 0);
   const int64_t first = parts.x + item;
   const float4* stat = reinterpret_cast<const float4*>(ws.stat) + first * 16;
-  const int y = blockIdx.y;
-  if (y < p.G) {
+  const int head_blocks = (p.G + kHeads - 1) / kHeads;
+  if (static_cast<int>(blockIdx.y) < head_blocks) {
+    const int head = blockIdx.y * kHeads + warp / SPLIT, share = warp % SPLIT;
+    const bool on = head < p.G;
     float rw = kNoRef, rs = kNoRef;
-    for (int i = lane; i < parts.y; i += 32) {
-      const float4 s = stat[i * 16 + y];
-      rw = fmaxf(rw, s.x);
-      rs = fmaxf(rs, s.y);
-    }
+    if (on)
+      for (int i = lane; i < parts.y; i += 32) {
+        const float4 s = stat[i * 16 + head];
+        rw = fmaxf(rw, s.x);
+        rs = fmaxf(rs, s.y);
+      }
     rw = warp_max(rw);
     rs = warp_max(rs);
     float acc[D / 32], l = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+    if (on) {
 #pragma unroll 4
-    for (int i = warp; i < parts.y; i += kMergeWarps) {
-      const float4 s = stat[i * 16 + y];
-      const float* row = ws.sum + ((first + i) * p.G + y) * D;
-      const float f = ex2(s.x - rw);
-      l += s.z * ex2(s.y - rs);
+      for (int i = share; i < parts.y; i += SPLIT) {
+        const float4 s = stat[i * 16 + head];
+        const float* row = ws.sum + ((first + i) * p.G + head) * D;
+        const float f = ex2(s.x - rw);
+        l += s.z * ex2(s.y - rs);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) acc[j] += f * row[j * 32 + lane];
-    }
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) s_sum[warp][j * 32 + lane] = acc[j];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (tid < D) {
-      float sum = 0.f, den = 0.f;
-#pragma unroll
-      for (int k = 0; k < kMergeWarps; ++k) {
-        sum += s_sum[k][tid];
-        den += s_l[k];
+        for (int j = 0; j < D / 32; ++j) acc[j] += f * row[j * 32 + lane];
       }
-      const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + y;
-      // sum is in units of 2^(rw - 14), den in units of 2^rs
-      store_out(out + row * D + dim_of<D>(tid), den == 0.f ? 0.f : sum / den * ex2(rw - kWeightExp - rs));
-      if (lse && tid == 0) lse[row] = den == 0.f ? -CUDART_INF_F : (rs + log2f(den)) * kLn2;
+    }
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) s_sum[warp][j * 32 + lane] = acc[j];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (share == 0) {
+        for (int k = 1; k < SPLIT; ++k) {
+          l += s_l[warp + k];
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) acc[j] += s_sum[warp + k][j * 32 + lane];
+        }
+      }
+    }
+    if (on && share == 0) {
+      const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + head;
+      // acc is in units of 2^(rw - 14), l in units of 2^rs
+      const float scale = l == 0.f ? 0.f : ex2(rw - kWeightExp - rs) / l;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+        store_out(out + row * D + dim_of<D>(j * 32 + lane), l == 0.f ? 0.f : acc[j] * scale);
+      if (lse && lane == 0) lse[row] = l == 0.f ? -CUDART_INF_F : (rs + log2f(l)) * kLn2;
     }
   } else {
-    const int e0 = (y - p.G) * kMergeEntries;
+    const int e0 = (static_cast<int>(blockIdx.y) - head_blocks) * kMergeEntries;
     if (e0 < units) {
       for (int head = warp; head < p.G; head += kMergeWarps) {
         float rs = kNoRef, l = 0.f;
@@ -920,7 +951,7 @@ int heads_rounded(const LayerParams& p) { return p.G <= 4 ? 4 : p.G <= 8 ? 8 : 1
 // Scratch layout; base may be null (sizes only).
 size_t layout(const LayerParams& p, int max_groups, bool weight, char* base, Workspace* ws) {
   const size_t items = static_cast<size_t>(p.B) * p.Hkv;
-  const size_t parts = items + static_cast<size_t>(device_sm_count()) * ctas_per_sm(heads_rounded(p));
+  const size_t parts = items + static_cast<size_t>(device_sm_count()) * ctas_per_sm(heads_rounded(p)) * kWarps;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* x = base + at;
@@ -945,11 +976,16 @@ cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void
   if (group_idx) most = std::min(most, static_cast<int64_t>(p.sink + p.local + 1) * p.Ng) + p.kg + 1;
   const int64_t slices = (items * (most + kItemCost) + kMinSlice - 1) / kMinSlice;
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(GM);
-  const unsigned grid = static_cast<unsigned>(slices < resident ? slices : resident);
-  const size_t smem = kWarps * kStages * kTile * Tile<D>::kUnitBytes + (group_idx ? p.kg * sizeof(int) : 0);
-  cudaError_t e = ensure_smem<quant_attend_kernel<T, D, FORMAT, GM>>(smem);
+  const unsigned grid = static_cast<unsigned>(std::min((slices + kWarps - 1) / kWarps, resident));
+  const size_t smem = 1024 + kWarps * (kStages * kTile * Tile<D>::kUnitBytes + (group_idx ? p.kg * sizeof(int) : 0));
+  CUtensorMap map_k, map_v;
+  cudaError_t e = make_byte_map(&map_k, qc.k, qc.n_slots * kQuantGroup, D, kQuantGroup);
+  if (e == cudaSuccess) e = make_byte_map(&map_v, qc.v, qc.n_slots * kQuantGroup, D, kQuantGroup);
   if (e != cudaSuccess) return e;
-  return launch_pdl(quant_attend_kernel<T, D, FORMAT, GM>, dim3(grid), dim3(kThreads), smem, s, 1, p, qc, static_cast<const T*>(q), pos,
+  e = ensure_smem<quant_attend_kernel<T, D, FORMAT, GM>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(quant_attend_kernel<T, D, FORMAT, GM>, dim3(grid), dim3(kThreads), smem, s, 1, map_k, map_v,
+                    p, qc, static_cast<const T*>(q), pos,
                     group_idx, ws, err);
 }
 
@@ -973,14 +1009,25 @@ cudaError_t launch_t(const LayerParams& p, const QuantCache& qc, const void* q, 
                    : launch_g<T, 128, kQuantE4m3>(p, qc, q, pos, gi, ws, err, s);
 }
 
+template <int D, typename TO, int SPLIT>
+cudaError_t launch_merge_split(const LayerParams& p, const QuantCache& qc, const int64_t* pos,
+                               const Workspace& ws, const int32_t* group_idx, const float* weight_in,
+                               float* weight_out, void* out, float* lse, cudaStream_t s) {
+  constexpr int threads = merge_warps(SPLIT) * 32, heads = merge_warps(SPLIT) / SPLIT;
+  const int blocks = (p.G + heads - 1) / heads + (weight_out ? (qc.max_groups + kMergeEntries - 1) / kMergeEntries : 0);
+  return launch_pdl(quant_merge_kernel<D, TO, SPLIT>, dim3(static_cast<unsigned>(p.B * p.Hkv), blocks),
+                    dim3(threads), 0, s, 1, p, qc, pos, ws, group_idx, weight_in, weight_out,
+                    static_cast<TO*>(out), lse);
+}
+
+// Few items have many partials each: a block per head; many items: a warp per head.
 template <int D, typename TO>
 cudaError_t launch_merge(const LayerParams& p, const QuantCache& qc, const int64_t* pos,
-                         const Workspace& ws, const int32_t* group_idx, const float* weight_in,
-                         float* weight_out, void* out, float* lse, cudaStream_t s) {
-  const int blocks = weight_out ? (qc.max_groups + kMergeEntries - 1) / kMergeEntries : 0;
-  return launch_pdl(quant_merge_kernel<D, TO>, dim3(static_cast<unsigned>(p.B * p.Hkv), p.G + blocks),
-                    dim3(kMergeThreads), 0, s, 1, p, qc, pos, ws, group_idx, weight_in, weight_out,
-                    static_cast<TO*>(out), lse);
+                         const Workspace& ws, const int32_t* gi, const float* wi, float* wo, void* out,
+                         float* lse, cudaStream_t s) {
+  return p.B * p.Hkv < device_sm_count()
+             ? launch_merge_split<D, TO, 32>(p, qc, pos, ws, gi, wi, wo, out, lse, s)
+             : launch_merge_split<D, TO, 1>(p, qc, pos, ws, gi, wi, wo, out, lse, s);
 }
 
 }  // namespace

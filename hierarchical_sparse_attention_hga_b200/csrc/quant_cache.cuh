@@ -16,6 +16,7 @@ namespace hga {
 
 constexpr int kQuantGroup = 16;  // tokens per group (cfg group is 16)
 constexpr int kQuantMaxGroups = 1 << 20;  // table entries per (sequence, KV head)
+constexpr int64_t kQuantMaxSlots = (1 << 27) - 1;  // a slot's first row is an int32 coordinate
 
 struct QuantCache {
   uint8_t* k;

@@ -129,7 +129,7 @@ typedef struct hga_quant_cache {
   void* v_tail;
   const int32_t* table;   /* device [B, Hkv, max_groups] */
   const int32_t* evicted; /* device [B, Hkv], or NULL */
-  int64_t n_slots;        /* slots in the pool (below 2^31) */
+  int64_t n_slots;        /* slots in the pool (below 2^27) */
   int32_t max_groups;     /* table entries per (sequence, KV head), at most 2^20 */
   int32_t format;         /* hga_quant_format */
 } hga_quant_cache;

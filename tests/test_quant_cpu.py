@@ -118,7 +118,7 @@ def test_struct_layout():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(table=None), 1), (dict(format=2), 1), (dict(max_groups=0), 1), (dict(n_slots=0), 1),
-    (dict(max_groups=(1 << 20) + 1), 3), (dict(n_slots=1 << 31), 3), (dict(k=None), 1),
+    (dict(max_groups=(1 << 20) + 1), 3), (dict(n_slots=1 << 27), 3), (dict(k=None), 1),
     (dict(v_scale=None), 1), (dict(k_tail=None), 1), (dict(v=24), 1), (dict(v_tail=8), 1)])
 def test_a_cache_that_append_and_attend_refuse(kw, status):
     layer = B.Layer(**LAYER)
