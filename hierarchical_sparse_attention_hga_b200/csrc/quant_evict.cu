@@ -7,12 +7,14 @@
 // slots, so a stable partition of it (kept entries, then the freed ones, then
 // the ones that were free) evicts and hands the freed slots to later appends.
 //
-// One CTA per item, thread t owning a contiguous run of entries.  The weights
-// are read once into shared memory and become order-preserving integers; the
-// threshold (the smallest kept key) is found digit by digit with shared-memory
-// histograms, and one block scan of (above, equal) counts gives every entry its
-// place.  All reads of a row come before its first write, so the outputs may be
-// the inputs.
+// One CTA per item; 16 bytes an entry, so a call is a chain of latencies.  The
+// weights become order-preserving integers; the threshold (the smallest kept
+// key) is found in three digits of 11, 11 and 10 bits with shared-memory
+// histograms (the first digit holds sign, exponent and two more bits, so that
+// weights of one size do not all meet in one counter).  Then 32 entries at a
+// time become two masks (above, equal), one block scan over the masks' counts
+// gives each its place, and kept and freed entries are written in order.  All
+// reads of a row come before its first write, so the outputs may be the inputs.
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_cache.cuh"
@@ -20,7 +22,7 @@
 namespace hga {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kBins = 2048;
 
 // Larger key = kept first.  NaN counts as least; -0 and +0 are equal.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -29,146 +31,199 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-struct ScanSmem {
-  unsigned long long part[kThreads / 32];
-};
-
-// Exclusive block scan of a pair of counts packed in one 64-bit word.
-__device__ __forceinline__ unsigned long long block_exclusive(unsigned long long v, ScanSmem& sm) {
+// Exclusive block scan; `total` gets the sum.
+template <int NT, typename V>
+__device__ __forceinline__ V block_exclusive(V v, V* part, V& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long x = v;
+  V x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const V y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) sm.part[warp] = x;
+  __syncthreads();  // part may still be read from the last scan
+  if (lane == 31) part[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    unsigned long long s = lane < kThreads / 32 ? sm.part[lane] : 0ull;
+  V s = lane < NT / 32 ? part[lane] : V(0);  // every warp scans the warps' sums
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    if (lane < kThreads / 32) sm.part[lane] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const V y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();
-  return x - v + (warp ? sm.part[warp - 1] : 0ull);
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const V before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  return x - v + (warp ? before : V(0));
 }
 
-__global__ void __launch_bounds__(kThreads)
+// Bytes of shared memory: one or both rows, then masks and places (or the histogram).
+__host__ __device__ inline int mask_words(int max_groups) { return (max_groups + 31) / 32; }
+__host__ __device__ inline size_t scratch_bytes(int max_groups) {
+  const size_t places = static_cast<size_t>(mask_words(max_groups)) * 8;
+  return mask_words(max_groups) * 8ull + (places > kBins * 4 ? places : kBins * 4);
+}
+size_t smem_bytes(int max_groups, int rows) {
+  return (static_cast<size_t>(max_groups) * rows * 4 + 15) / 16 * 16 + scratch_bytes(max_groups);
+}
+
+// ROWS: rows in shared memory at a time (the weights, or the weights and the table).
+template <int NT, int ROWS>
+__global__ void __launch_bounds__(NT)
 quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* __restrict__ pos, int keep, int sink,
                    int recent, const float* weight_in, float* weight_out, int32_t* table_out,
                    int32_t* evicted_out, unsigned* err) {
-  extern __shared__ uint32_t s_row[];  // [max_groups]: the weights, then the table
-  __shared__ unsigned s_hist[256];
-  __shared__ ScanSmem s_scan;
-  __shared__ uint32_t s_prefix;
+  extern __shared__ __align__(16) uint32_t s_mem[];
+  __shared__ unsigned long long s_part[NT / 32];
+  __shared__ unsigned s_part32[NT / 32];
+  __shared__ uint32_t s_digit;
   __shared__ int s_need;
+  const int max_groups = qc.max_groups, words = mask_words(max_groups);
+  uint32_t* s_weight = s_mem;
+  uint32_t* s_table = ROWS == 2 ? s_mem + max_groups : s_mem;
+  uint32_t* s_above = s_mem + (max_groups * ROWS + 3) / 4 * 4;
+  uint32_t* s_equal = s_above + words;
+  unsigned long long* s_place = reinterpret_cast<unsigned long long*>(s_above + (2 * words));
+  unsigned* s_hist = reinterpret_cast<unsigned*>(s_place);
   const int64_t item = blockIdx.x;
-  const int tid = threadIdx.x;
-  pdl_wait();
-
-  const QuantItem it = quant_item(qc, pos[item / Hkv], item, tid == 0 ? err : nullptr);
-  const int n = it.closed, max_groups = qc.max_groups;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* w_in = weight_in + item * max_groups;
   float* w_out = weight_out + item * max_groups;
   const int32_t* t_in = qc.table + item * max_groups;
   int32_t* t_out = table_out + item * max_groups;
+  pdl_wait();
+
+  for (int i = tid; i < max_groups; i += NT) {
+    s_weight[i] = __float_as_uint(w_in[i]);
+    if (ROWS == 2) s_table[i] = static_cast<uint32_t>(t_in[i]);
+  }
+  const QuantItem it = quant_item(qc, pos[item / Hkv], item, tid == 0 ? err : nullptr);
   const int gone = qc.evicted ? qc.evicted[item] : 0;
-  if (!it.ok) {  // flagged: nothing is evicted
-    for (int i = tid; i < max_groups; i += kThreads) {
-      w_out[i] = w_in[i];
-      t_out[i] = t_in[i];
-    }
-    if (tid == 0) evicted_out[item] = gone;
-    return;
-  }
-  for (int i = tid; i < max_groups; i += kThreads) s_row[i] = __float_as_uint(w_in[i]);
-  __syncthreads();
-
-  const int lo = sink, hi = n - recent;   // candidates [lo, hi)
-  const bool evicts = n > keep;           // then hi - lo > keep - sink - recent >= 0
-  const int want = keep - sink - recent;  // candidates that stay
-  uint32_t threshold = 0xffffffffu;       // no finite or infinite weight has this key
+  const int n = it.closed;
+  const int lo = sink, hi = n - recent;      // candidates [lo, hi)
+  const bool evicts = n > keep;              // then hi - lo > keep - sink - recent >= 0
+  const int want = keep - sink - recent;     // candidates that stay
+  uint32_t threshold = 0xffffffffu;          // no weight has this key
   int ties = 0;
+  __syncthreads();
   if (evicts && want > 0) {
-    if (tid == 0) {
-      s_prefix = 0;
-      s_need = want;
-    }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) s_hist[tid] = 0;
+    uint32_t prefix = 0;
+    int need = want;
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+      const int bits = shift == 0 ? 10 : 11;
+      for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
       __syncthreads();
-      const uint32_t prefix = s_prefix;
-      for (int i = lo + tid; i < hi; i += kThreads) {
-        const uint32_t key = weight_key(__uint_as_float(s_row[i]));
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&s_hist[(key >> shift) & 255], 1u);
+      for (int i = lo + tid; i < hi; i += NT) {
+        const uint32_t key = weight_key(__uint_as_float(s_weight[i]));
+        if (shift == 21 || (key >> (shift + bits)) == (prefix >> (shift + bits)))
+          atomicAdd(&s_hist[(key >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (tid == 0) {
-        int need = s_need, d = 255;
-        while (static_cast<int>(s_hist[d]) < need) need -= s_hist[d--];
-        s_need = need;
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
+      // thread t holds the bins from the top: kBins - 1 - t * each and below
+      constexpr int kEach = kBins / NT;
+      unsigned mine = 0, total;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) mine += s_hist[kBins - 1 - tid * kEach - j];
+      unsigned before = block_exclusive<NT, unsigned>(mine, s_part32, total);
+      if (before < static_cast<unsigned>(need) && before + mine >= static_cast<unsigned>(need)) {
+        int j = 0;
+        unsigned c;
+        while (before + (c = s_hist[kBins - 1 - tid * kEach - j]) < static_cast<unsigned>(need)) {
+          before += c;
+          ++j;
+        }
+        s_digit = kBins - 1 - tid * kEach - j;
+        s_need = need - static_cast<int>(before);
       }
       __syncthreads();
+      prefix |= s_digit << shift;
+      need = s_need;
     }
-    threshold = s_prefix;
-    ties = s_need;  // entries equal to the threshold that stay, the earliest ones
+    threshold = prefix;
+    ties = need;  // entries equal to the threshold that stay, the earliest ones
+    __syncthreads();
   }
 
-  // thread t owns entries [i0, i1); an odd run length spreads the banks
-  const int run = ((max_groups + kThreads - 1) / kThreads) | 1;
-  const int i0 = min(tid * run, max_groups), i1 = min(i0 + run, max_groups);
-  unsigned long long mine = 0;  // low word: kept whatever the ties, high word: equal to the threshold
-  for (int i = i0; i < min(i1, n); ++i) {
-    if (!evicts || i < lo || i >= hi) {
-      mine += 1;
-    } else {
-      const uint32_t key = weight_key(__uint_as_float(s_row[i]));
-      if (key > threshold) mine += 1;
-      else if (key == threshold) mine += 1ull << 32;
-    }
-  }
-  const unsigned long long before = block_exclusive(mine, s_scan);
-  const int kept_n = evicts ? keep : n;
-  int kept = static_cast<int>(before & 0xffffffffu);
-  int equal = static_cast<int>(before >> 32);
-  int place = kept + min(equal, ties);  // kept entries before this thread's run
-  unsigned long long mask[2] = {0, 0};  // which of the run's entries are kept (run <= 97)
-  const int place0 = place;
-  for (int i = i0; i < i1; ++i) {
-    bool stay = i >= n;
+  for (int w = warp; w < words; w += NT / 32) {
+    const int i = w * 32 + lane;
+    bool above = false, equal = false;
     if (i < n) {
-      if (!evicts || i < lo || i >= hi) {
-        stay = true;
-      } else {
-        const uint32_t key = weight_key(__uint_as_float(s_row[i]));
-        stay = key > threshold || (key == threshold && equal++ < ties);
+      above = !evicts || i < lo || i >= hi;
+      if (!above) {
+        const uint32_t key = weight_key(__uint_as_float(s_weight[i]));
+        above = key > threshold;
+        equal = key == threshold;
       }
-      if (stay) w_out[place++] = __uint_as_float(s_row[i]);
     }
-    if (stay) mask[(i - i0) >> 6] |= 1ull << ((i - i0) & 63);
+    const unsigned a = __ballot_sync(0xffffffffu, above), e = __ballot_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      s_above[w] = a;
+      s_equal[w] = e;
+    }
   }
-  // the open group's weight follows the last kept one; entries behind it start at 0
-  for (int i = kept_n + tid; i < max_groups; i += kThreads)
-    w_out[i] = i == kept_n && n < max_groups ? __uint_as_float(s_row[n]) : 0.f;
+  __syncthreads();
+  // counts (above in the low word, equal in the high one) before each mask
+  unsigned long long carry = 0;
+  for (int w0 = 0; w0 < words; w0 += NT) {
+    const int w = w0 + tid;
+    const unsigned long long c =
+        w < words ? __popc(s_above[w]) | static_cast<unsigned long long>(__popc(s_equal[w])) << 32 : 0ull;
+    unsigned long long total;
+    const unsigned long long x = block_exclusive<NT, unsigned long long>(c, s_part, total);
+    if (w < words) s_place[w] = carry + x;
+    carry += total;
+  }
   __syncthreads();
 
-  for (int i = tid; i < max_groups; i += kThreads) s_row[i] = static_cast<uint32_t>(t_in[i]);
-  __syncthreads();
-  place = place0;
-  for (int i = i0; i < i1; ++i) {
-    const bool stay = mask[(i - i0) >> 6] >> ((i - i0) & 63) & 1;
-    int to = i;
-    if (i < n) to = stay ? place++ : kept_n + (i - place);
-    t_out[to] = static_cast<int32_t>(s_row[i]);
+  const int kept_n = evicts ? keep : n;
+  // Whether entry i stays and where it goes.  A flagged item is passed through.
+  auto place_of = [&](int w, bool& stay) {
+    const int i = w * 32 + lane;
+    const unsigned below = (1u << lane) - 1, a = s_above[w], e = s_equal[w];
+    const unsigned long long at = s_place[w];
+    const int equal = static_cast<int>(at >> 32) + __popc(e & below);
+    const int kept = static_cast<int>(at & 0xffffffffu) + __popc(a & below) + min(equal, ties);
+    stay = (a >> lane & 1) || ((e >> lane & 1) && equal < ties);
+    return i >= n ? i : stay ? kept : kept_n + (i - kept);
+  };
+  auto write_weights = [&]() {
+    for (int w = warp; w < words; w += NT / 32) {
+      const int i = w * 32 + lane;
+      bool stay;
+      const int to = place_of(w, stay);
+      if (i < n && stay) w_out[to] = __uint_as_float(s_weight[i]);
+    }
+    // the open group's weight follows the last kept one; entries behind it start at 0
+    for (int i = kept_n + tid; i < max_groups; i += NT)
+      w_out[i] = !it.ok ? __uint_as_float(s_weight[i]) : i == kept_n && n < max_groups ? __uint_as_float(s_weight[n]) : 0.f;
+  };
+  auto write_table = [&]() {
+    for (int w = warp; w < words; w += NT / 32) {
+      const int i = w * 32 + lane;
+      bool stay;
+      const int to = place_of(w, stay);
+      if (i < max_groups) t_out[to] = static_cast<int32_t>(s_table[i]);
+    }
+  };
+  write_weights();
+  if (ROWS == 1) {
+    __syncthreads();
+    for (int i = tid; i < max_groups; i += NT) s_table[i] = static_cast<uint32_t>(t_in[i]);
+    __syncthreads();
   }
+  write_table();
   if (tid == 0) evicted_out[item] = gone + (n - kept_n);
   pdl_trigger();
+}
+
+template <int NT, int ROWS>
+cudaError_t launch(const LayerParams& p, const QuantCache& qc, const int64_t* pos, int keep, int sink,
+                   int recent, const float* weight_in, float* weight_out, int32_t* table_out,
+                   int32_t* evicted_out, unsigned* err, cudaStream_t s) {
+  const size_t smem = smem_bytes(qc.max_groups, ROWS);
+  cudaError_t e = ensure_smem<quant_evict_kernel<NT, ROWS>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(quant_evict_kernel<NT, ROWS>, dim3(static_cast<unsigned>(p.B * p.Hkv)), dim3(NT),
+                    smem, s, 1, p.Hkv, qc, pos, keep, sink, recent, weight_in, weight_out, table_out,
+                    evicted_out, err);
 }
 
 }  // namespace
@@ -177,12 +232,10 @@ cudaError_t launch_quant_evict(const LayerParams& p, const QuantCache& qc, const
                                int keep, int sink, int recent, const float* weight_in,
                                float* weight_out, int32_t* table_out, int32_t* evicted_out,
                                unsigned* err, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(qc.max_groups) * sizeof(uint32_t);
-  cudaError_t e = ensure_smem<quant_evict_kernel>(smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(quant_evict_kernel, dim3(static_cast<unsigned>(p.B * p.Hkv)), dim3(kThreads),
-                    smem, s, 1, p.Hkv, qc, pos, keep, sink, recent, weight_in, weight_out,
-                    table_out, evicted_out, err);
+  auto* kernel = launch<256, 2>;
+  if (qc.max_groups > 1024) kernel = launch<1024, 2>;
+  if (smem_bytes(qc.max_groups, 2) > 220 * 1024) kernel = launch<1024, 1>;
+  return kernel(p, qc, pos, keep, sink, recent, weight_in, weight_out, table_out, evicted_out, err, s);
 }
 
 }  // namespace hga
