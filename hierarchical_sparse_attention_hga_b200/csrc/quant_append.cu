@@ -15,9 +15,15 @@
 // groups closed by earlier calls are their stored rows times 16 (exact: a power
 // of two), so token-by-token and batch appends give the batch builder's bits.
 //
-// One CTA per chunk (looping), one warp per (group, tensor): a lane owns the
-// pairs (i, i + D/2) that the summary needs and holds the group's 16 rows of
-// them in registers, so every row is read once.
+// One CTA per chunk (looping), one warp per (group, tensor), which reads each row
+// once into registers: lane l holds E = D / 32 consecutive dimensions of all 16
+// rows, so a row is one load and its codes one store of the warp.  The rotation
+// of the summaries needs dimensions i and i + D/2 together; they are held by lanes
+// l and l + 16, which trade half of their elements (one shuffle a row).
+// Bound by HBM in a prompt (3 D bytes a token and tensor for bf16), by latency in
+// a decode step.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_cache.cuh"
@@ -28,16 +34,105 @@ namespace {
 
 using summ::kGroup;
 
-template <int FORMAT>
-__device__ __forceinline__ uint32_t quantise2(float a, float b) {  // two codes, a in the low byte
-  if (FORMAT == kQuantInt8) {
-    // |a|, |b| <= 127 (1 + 2^-23): rounds to at most 127
-    const int ia = __float2int_rn(a), ib = __float2int_rn(b);
-    return (ia & 0xff) | ((ib & 0xff) << 8);
+// E consecutive elements of a row as they are stored.
+template <typename T, int E> struct Piece;
+template <> struct Piece<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  // |x| of all elements as float bits: integer order, NaN above infinity
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
+    return max(max(a << 16, a & 0xffff0000u), max(b << 16, b & 0xffff0000u));
+  }
+  // the half of the elements that the partner lane needs, and back
+  __device__ __forceinline__ void trade(bool upper, float (&x)[2], float (&y)[2]) const {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16), mine = upper ? v.y : v.x;
+    const uint32_t wx = upper ? other : mine, wy = upper ? mine : other;
+    x[0] = __uint_as_float(wx << 16); x[1] = __uint_as_float(wx & 0xffff0000u);
+    y[0] = __uint_as_float(wy << 16); y[1] = __uint_as_float(wy & 0xffff0000u);
+  }
+};
+template <> struct Piece<__nv_bfloat16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t a = v & 0x7fff7fffu;
+    return max(a << 16, a & 0xffff0000u);
+  }
+  __device__ __forceinline__ void trade(bool upper, float (&x)[1], float (&y)[1]) const {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, v, 16);
+    // lane l takes the pair of its first element, lane l + 16 that of its second
+    x[0] = __uint_as_float(upper ? other & 0xffff0000u : v << 16);
+    y[0] = __uint_as_float(upper ? v & 0xffff0000u : other << 16);
+  }
+};
+template <> struct Piece<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(__float_as_uint(v.x) & m, __float_as_uint(v.y) & m), max(__float_as_uint(v.z) & m, __float_as_uint(v.w) & m));
+  }
+  __device__ __forceinline__ void trade(bool upper, float (&x)[2], float (&y)[2]) const {
+    const float o0 = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.z, 16);
+    const float o1 = __shfl_xor_sync(0xffffffffu, upper ? v.y : v.w, 16);
+    x[0] = upper ? o0 : v.x; x[1] = upper ? o1 : v.y;
+    y[0] = upper ? v.z : o0; y[1] = upper ? v.w : o1;
+  }
+};
+template <> struct Piece<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ float at(int i) const { return i ? v.y : v.x; }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu);
+  }
+  __device__ __forceinline__ void trade(bool upper, float (&x)[1], float (&y)[1]) const {
+    const float o = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
+    x[0] = upper ? o : v.x;
+    y[0] = upper ? v.y : o;
+  }
+};
+
+// E codes, the first in the lowest byte.
+template <int FORMAT, int E>
+__device__ __forceinline__ uint32_t quantise(const float (&y)[E]) {
+  uint32_t r = 0;
+  if (FORMAT == kQuantInt8) {
+    // |y| <= 127 (1 + 2^-23): adding 1.5 * 2^23 rounds to the nearest even integer,
+    // whose low byte is the code
+    uint32_t w[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+    r = __byte_perm(w[0], w[1], 0x0040);
+    if (E == 4) r = __byte_perm(r, __byte_perm(w[E - 2], w[E - 1], 0x0040), 0x5410);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      uint16_t h;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y[i + 1]), "f"(y[i]));
+      r |= static_cast<uint32_t>(h) << (8 * i);
+    }
+  }
   return r;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, uint32_t r, std::integral_constant<int, 4>) {
+  *reinterpret_cast<uint32_t*>(p) = r;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, uint32_t r, std::integral_constant<int, 2>) {
+  *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r);
+}
+
+// A barrier of the K warps alone.
+__device__ __forceinline__ void k_barrier(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
 
 template <typename T, int D, int FORMAT>
@@ -46,7 +141,7 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
                     const T* __restrict__ v_new, int n_new, const int32_t* __restrict__ counts,
                     const int64_t* __restrict__ pos, float* __restrict__ chunk_sum,
                     float* __restrict__ group_sum, unsigned* err) {
-  constexpr int P = D / 2, PPL = P / 32;
+  constexpr int P = D / 2, E = D / 32, H = E / 2;  // H: pairs of a lane
   constexpr float kPeak = FORMAT == kQuantInt8 ? 127.f : 448.f;
   extern __shared__ float2 smem_tab[];
   __shared__ float s_gsum[8][D];
@@ -71,101 +166,105 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
   const int n_lo = P - p.n_high;
   const bool is_v = warp >= p.Ng;
   const int w = is_v ? warp - p.Ng : warp;
-  const T* src = (is_v ? v_new : k_new) + item * n_new * D;
-  T* tail = static_cast<T*>(is_v ? qc.v_tail : qc.k_tail) + item * kGroup * D;
-  uint8_t* codes = is_v ? qc.v : qc.k;
-  float* scales = is_v ? qc.v_scale : qc.k_scale;
 
   if (u_end > u0) {
-    if (sums) {
+    const int64_t c_last = (u_end - 1) / p.Ng;
+    if (sums && u0 / p.Ng + blockIdx.y <= c_last) {
       for (int i = threadIdx.x; i < summ::table_entries(p, D); i += blockDim.x)
         smem_tab[i] = summ::table_entry(p, D, i);
       __syncthreads();
     }
-    const int64_t c_last = (u_end - 1) / p.Ng;
+    const T* src = (is_v ? v_new : k_new) + item * n_new * D + lane * E;
+    const T* tail = static_cast<const T*>(is_v ? qc.v_tail : qc.k_tail) + item * kGroup * D + lane * E;
+    uint8_t* codes = is_v ? qc.v : qc.k;
+    float* scales = is_v ? qc.v_scale : qc.k_scale;
+    // this lane's pairs: dims pair + j and pair + j + D/2
+    const bool upper = lane >= 16;
+    const int pair = (lane & 15) * E + (upper ? H : 0);
     for (int64_t c = u0 / p.Ng + blockIdx.y; c <= c_last; c += gridDim.y) {
       const int64_t u = c * p.Ng + w;
       const bool in_table = u < qc.max_groups;  // the summary tables' capacity
       if (u >= u0 && u < u_end) {
-        float x[kGroup][PPL], y[kGroup][PPL];
+        const int32_t slot = qc.table[item * qc.max_groups + (u - gone)];
+        Piece<T, E> x[kGroup];
         uint32_t top = 0;
 #pragma unroll
         for (int r = 0; r < kGroup; ++r) {
           const int64_t i = u * kGroup + r - p0;
-          const T* row = (i >= 0 ? src + i * D : tail + r * D) + lane * PPL;
-#pragma unroll
-          for (int e = 0; e < PPL; ++e) {
-            x[r][e] = to_f32(row[e]);
-            y[r][e] = to_f32(row[P + e]);
-          }
+          x[r].load(i >= 0 ? src + i * D : tail + r * D);
         }
 #pragma unroll
-        for (int r = 0; r < kGroup; ++r)
-#pragma unroll
-          for (int e = 0; e < PPL; ++e)
-            top = max(top, max(__float_as_uint(x[r][e]) & 0x7fffffffu,
-                               __float_as_uint(y[r][e]) & 0x7fffffffu));
-        top = __reduce_max_sync(0xffffffffu, top);  // as integers, NaN > inf > finite
+        for (int r = 0; r < kGroup; ++r) top = max(top, x[r].top());
+        top = __reduce_max_sync(0xffffffffu, top);
         const float amax = __uint_as_float(top);
         const bool finite = top < 0x7f800000u;
         const bool some = finite && amax >= 0x1p-100f;
         const float inverse = some ? __fdiv_rn(kPeak, amax) : 0.f;
         const float scale = some ? __fdiv_rn(amax, kPeak) : (finite ? 0.f : CUDART_NAN_F);
-        const int32_t slot = qc.table[item * qc.max_groups + (u - gone)];
         if (slot >= 0 && slot < qc.n_slots) {
-          uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * PPL;
+          uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * E;
 #pragma unroll
           for (int r = 0; r < kGroup; ++r) {
-            if constexpr (PPL == 2) {
-              const uint32_t cx = finite ? quantise2<FORMAT>(__fmul_rn(x[r][0], inverse), __fmul_rn(x[r][1], inverse)) : 0u;
-              const uint32_t cy = finite ? quantise2<FORMAT>(__fmul_rn(y[r][0], inverse), __fmul_rn(y[r][1], inverse)) : 0u;
-              *reinterpret_cast<uint16_t*>(dst + r * D) = static_cast<uint16_t>(cx);
-              *reinterpret_cast<uint16_t*>(dst + r * D + P) = static_cast<uint16_t>(cy);
-            } else {
-              const uint32_t cxy = finite ? quantise2<FORMAT>(__fmul_rn(x[r][0], inverse), __fmul_rn(y[r][0], inverse)) : 0u;
-              dst[r * D] = static_cast<uint8_t>(cxy);
-              dst[r * D + P] = static_cast<uint8_t>(cxy >> 8);
-            }
+            float y[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) y[i] = __fmul_rn(x[r].at(i), inverse);
+            store_codes(dst + r * D, finite ? quantise<FORMAT, E>(y) : 0u, std::integral_constant<int, E>());
           }
           if (lane == 0) scales[slot] = scale;
         } else if (lane == 0) {
           flag_error(err, kErrPage);
         }
         if (sums && !is_v) {
-          float gx[PPL], gy[PPL];
-          summ::group_raw_sum<PPL>(x, y, smem_tab, p.n_high, n_lo, lane, gx, gy);
+          float gx[H], gy[H];
+#pragma unroll
+          for (int j = 0; j < H; ++j) gx[j] = gy[j] = 0.f;
+#pragma unroll
+          for (int r = 0; r < kGroup; ++r) {  // the batch builder's order and roundings
+            float px[H], py[H];
+            x[r].trade(upper, px, py);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+              const int i = pair + j;
+              if (i < p.n_high) {
+                gx[j] = __fadd_rn(gx[j], px[j]);
+                gy[j] = __fadd_rn(gy[j], py[j]);
+              } else {
+                summ::add_rotated(gx[j], gy[j], px[j], py[j], smem_tab[r * n_lo + i - p.n_high]);
+              }
+            }
+          }
           if (in_table) {
             float* dst = group_sum + (item * qc.max_groups + u) * D;
 #pragma unroll
-            for (int e = 0; e < PPL; ++e) {
-              dst[lane * PPL + e] = __fmul_rn(gx[e], 1.0f / kGroup);
-              dst[P + lane * PPL + e] = __fmul_rn(gy[e], 1.0f / kGroup);
+            for (int j = 0; j < H; ++j) {
+              dst[pair + j] = __fmul_rn(gx[j], 1.0f / kGroup);
+              dst[P + pair + j] = __fmul_rn(gy[j], 1.0f / kGroup);
             }
           } else if (lane == 0) {
             flag_error(err, kErrPos);
           }
 #pragma unroll
-          for (int e = 0; e < PPL; ++e) {
-            s_gsum[w][lane * PPL + e] = gx[e];
-            s_gsum[w][P + lane * PPL + e] = gy[e];
+          for (int j = 0; j < H; ++j) {
+            s_gsum[w][pair + j] = gx[j];
+            s_gsum[w][P + pair + j] = gy[j];
           }
         }
       } else if (sums && !is_v && u < u0 && in_table) {  // a group an earlier call closed
         const float* row = group_sum + (item * qc.max_groups + u) * D;
         for (int i = lane; i < D; i += 32) s_gsum[w][i] = __fmul_rn(row[i], static_cast<float>(kGroup));
       }
-      if (sums && (c + 1) * p.Ng <= u_end) {  // the chunk closes: uniform over the CTA
-        __syncthreads();
+      if (sums && !is_v && (c + 1) * p.Ng <= u_end) {  // the chunk closes: uniform over the K warps
+        k_barrier(p.Ng * 32);
         if (c < p.n_chunks) {
           const float inv_c = 1.0f / p.C;
           float* dst = chunk_sum + (item * p.n_chunks + c) * D;
-          for (int i = threadIdx.x; i < P; i += blockDim.x) {
+          for (int i = threadIdx.x; i < P; i += p.Ng * 32) {
             const float2 sc = summ::chunk_pair<D>(s_gsum, smem_tab + kGroup * n_lo, p.Ng, p.n_high, n_lo, i);
             dst[i] = __fmul_rn(sc.x, inv_c);
             dst[P + i] = __fmul_rn(sc.y, inv_c);
           }
         }
-        __syncthreads();
+        k_barrier(p.Ng * 32);
       }
     }
   }
@@ -175,11 +274,12 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
     __syncthreads();
     const int64_t t0 = max(p0, u_end * kGroup);
     const int rows = static_cast<int>(pb + 1 - t0);
-    for (int i = threadIdx.x; i < 2 * rows * D; i += blockDim.x) {
-      const int which = i / (rows * D), j = i % (rows * D), r = j / D, d = j % D;
-      const T* from = (which ? v_new : k_new) + (item * n_new + (t0 - p0) + r) * D + d;
-      T* to = static_cast<T*>(which ? qc.v_tail : qc.k_tail) + (item * kGroup + ((t0 + r) & 15)) * D + d;
-      *to = *from;
+    const T* from = (is_v ? v_new : k_new) + (item * n_new + (t0 - p0)) * D;
+    T* to = static_cast<T*>(is_v ? qc.v_tail : qc.k_tail) + (item * kGroup + (t0 & 15)) * D;
+    for (int r = w; r < rows; r += p.Ng) {
+      Piece<T, E> x;
+      x.load(from + r * D + lane * E);
+      *reinterpret_cast<Piece<T, E>*>(to + r * D + lane * E) = x;
     }
   }
   pdl_trigger();
