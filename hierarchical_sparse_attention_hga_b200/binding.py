@@ -143,10 +143,12 @@ def _ptr(x):
     """Raw address of a tensor (or an int address, or None)."""
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if not x.flags["C_CONTIGUOUS"]:  # a numpy array (host-side calls)
         raise ValueError("host arrays passed to the library must be C-contiguous")
     return x.ctypes.data
@@ -155,6 +157,10 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            # the same handle without building a Stream object (3.3 us a call)
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
