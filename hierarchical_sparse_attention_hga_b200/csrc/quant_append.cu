@@ -15,13 +15,15 @@
 // groups closed by earlier calls are their stored rows times 16 (exact: a power
 // of two), so token-by-token and batch appends give the batch builder's bits.
 //
-// One CTA per chunk (looping), one warp per (group, tensor), which reads each row
-// once into registers: lane l holds E = D / 32 consecutive dimensions of all 16
-// rows, so a row is one load and its codes one store of the warp.  The rotation
-// of the summaries needs dimensions i and i + D/2 together; they are held by lanes
-// l and l + 16, which trade half of their elements (one shuffle a row).
+// One CTA per chunk (looping), one warp per group, which loads the group's K and V
+// rows at once and holds them in registers: lane l has E = D / 32 consecutive
+// dimensions of all 16 rows, so a row is one load and its codes one store of the
+// warp.  The rotation of the summaries needs dimensions i and i + D/2 together;
+// they are held by lanes l and l + 16, which trade half of their elements (one
+// shuffle a row).
 // Bound by HBM in a prompt (3 D bytes a token and tensor for bf16), by latency in
 // a decode step.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -34,6 +36,68 @@ namespace {
 
 using summ::kGroup;
 
+constexpr int kCtas4 = 4, kCtas8 = 2;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two floats in one register pair; each half of an operation is rounded as the
+// scalar one.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Sums of H rotated pairs over a group's rows, with the batch builder's roundings
+// (summ::add_rotated): x += x c - y s, y += x s + y c.  High-frequency pairs have
+// (c, s) = (1, 0), which leaves the bits of finite rows as a plain sum has them.
+// table: per row and H pairs, cosines then sines.
+template <int H> struct RotatedSum;
+template <> struct RotatedSum<2> {
+  uint64_t x = 0, y = 0;
+  __device__ __forceinline__ void add(const float (&a)[2], const float (&b)[2], const float* table) {
+    const float4 t = *reinterpret_cast<const float4*>(table);
+    const uint64_t c = pack2(t.x, t.y), s = pack2(t.z, t.w), a2 = pack2(a[0], a[1]), b2 = pack2(b[0], b[1]);
+    x = add2(x, fma2(a2, c, mul2(b2, s ^ 0x8000000080000000ull)));
+    y = add2(y, fma2(a2, s, mul2(b2, c)));
+  }
+  __device__ __forceinline__ void get(float (&a)[2], float (&b)[2]) const {
+    const float2 u = unpack2(x), v = unpack2(y);
+    a[0] = u.x; a[1] = u.y; b[0] = v.x; b[1] = v.y;
+  }
+};
+template <> struct RotatedSum<1> {
+  float x = 0.f, y = 0.f;
+  __device__ __forceinline__ void add(const float (&a)[1], const float (&b)[1], const float* table) {
+    summ::add_rotated(x, y, a[0], b[0], *reinterpret_cast<const float2*>(table));
+  }
+  __device__ __forceinline__ void get(float (&a)[1], float (&b)[1]) const { a[0] = x; b[0] = y; }
+};
+
 // E consecutive elements of a row as they are stored.
 template <typename T, int E> struct Piece;
 template <> struct Piece<__nv_bfloat16, 4> {
@@ -43,11 +107,11 @@ template <> struct Piece<__nv_bfloat16, 4> {
     const uint32_t w = i < 2 ? v.x : v.y;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
-  // |x| of all elements as float bits: integer order, NaN above infinity
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
-    return max(max(a << 16, a & 0xffff0000u), max(b << 16, b & 0xffff0000u));
+  // the largest |x| so far, as bits: integer order, NaN above infinity
+  static __device__ __forceinline__ void raise(uint32_t& top, const Piece& x) {
+    top = max_u16x2(max_u16x2(top, x.v.x & 0x7fff7fffu), x.v.y & 0x7fff7fffu);
   }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t top) { return max(top << 16, top & 0xffff0000u); }
   // the half of the elements that the partner lane needs, and back
   __device__ __forceinline__ void trade(bool upper, float (&x)[2], float (&y)[2]) const {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16), mine = upper ? v.y : v.x;
@@ -60,10 +124,8 @@ template <> struct Piece<__nv_bfloat16, 2> {
   uint32_t v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t a = v & 0x7fff7fffu;
-    return max(a << 16, a & 0xffff0000u);
-  }
+  static __device__ __forceinline__ void raise(uint32_t& top, const Piece& x) { top = max_u16x2(top, x.v & 0x7fff7fffu); }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t top) { return max(top << 16, top & 0xffff0000u); }
   __device__ __forceinline__ void trade(bool upper, float (&x)[1], float (&y)[1]) const {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, v, 16);
     // lane l takes the pair of its first element, lane l + 16 that of its second
@@ -75,10 +137,11 @@ template <> struct Piece<float, 4> {
   float4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t m = 0x7fffffffu;
-    return max(max(__float_as_uint(v.x) & m, __float_as_uint(v.y) & m), max(__float_as_uint(v.z) & m, __float_as_uint(v.w) & m));
+  static __device__ __forceinline__ void raise(uint32_t& top, const Piece& x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x.at(i)) & 0x7fffffffu);
   }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t top) { return top; }
   __device__ __forceinline__ void trade(bool upper, float (&x)[2], float (&y)[2]) const {
     const float o0 = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.z, 16);
     const float o1 = __shfl_xor_sync(0xffffffffu, upper ? v.y : v.w, 16);
@@ -90,9 +153,10 @@ template <> struct Piece<float, 2> {
   float2 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
   __device__ __forceinline__ float at(int i) const { return i ? v.y : v.x; }
-  __device__ __forceinline__ uint32_t top() const {
-    return max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu);
+  static __device__ __forceinline__ void raise(uint32_t& top, const Piece& x) {
+    top = max(top, max(__float_as_uint(x.v.x) & 0x7fffffffu, __float_as_uint(x.v.y) & 0x7fffffffu));
   }
+  static __device__ __forceinline__ uint32_t float_bits(uint32_t top) { return top; }
   __device__ __forceinline__ void trade(bool upper, float (&x)[1], float (&y)[1]) const {
     const float o = __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
     x[0] = upper ? o : v.x;
@@ -130,21 +194,53 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint32_t r, std::integra
   *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r);
 }
 
-// A barrier of the K warps alone.
-__device__ __forceinline__ void k_barrier(int threads) {
-  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+// Resident CTAs per SM of 32 * NG threads that the launch bounds ask for.
+constexpr int ctas_per_sm(int ng) { return ng == 4 ? kCtas4 : kCtas8; }
+
+// Codes and scale of one group's rows (a lane's part), stored at the slot.
+template <typename T, int D, int FORMAT>
+__device__ __forceinline__ void write_group(const Piece<T, D / 32> (&x)[kGroup], uint8_t* codes,
+                                            float* scales, int32_t slot) {
+  constexpr int E = D / 32;
+  constexpr float kPeak = FORMAT == kQuantInt8 ? 127.f : 448.f;
+  const int lane = threadIdx.x & 31;
+  uint32_t top = 0;
+#pragma unroll
+  for (int r = 0; r < kGroup; ++r) Piece<T, E>::raise(top, x[r]);
+  top = __reduce_max_sync(0xffffffffu, Piece<T, E>::float_bits(top));
+  const float amax = __uint_as_float(top);
+  const bool finite = top < 0x7f800000u;
+  const bool some = finite && amax >= 0x1p-100f;
+  const float inverse = some ? __fdiv_rn(kPeak, amax) : 0.f;
+  const float scale = some ? __fdiv_rn(amax, kPeak) : (finite ? 0.f : CUDART_NAN_F);
+  const uint64_t inverse2 = pack2(inverse, inverse);
+  uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * E;
+#pragma unroll
+  for (int r = 0; r < kGroup; ++r) {
+    float y[E];
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float2 t = unpack2(mul2(pack2(x[r].at(i), x[r].at(i + 1)), inverse2));
+      y[i] = t.x;
+      y[i + 1] = t.y;
+    }
+    store_codes(dst + r * D, finite ? quantise<FORMAT, E>(y) : 0u, std::integral_constant<int, E>());
+  }
+  if (lane == 0) scales[slot] = scale;
 }
 
-template <typename T, int D, int FORMAT>
-__global__ void __launch_bounds__(512)
+template <typename T, int D, int FORMAT, int NG>
+__global__ void __launch_bounds__(32 * NG, ctas_per_sm(NG))
 quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
                     const T* __restrict__ v_new, int n_new, const int32_t* __restrict__ counts,
                     const int64_t* __restrict__ pos, float* __restrict__ chunk_sum,
                     float* __restrict__ group_sum, unsigned* err) {
   constexpr int P = D / 2, E = D / 32, H = E / 2;  // H: pairs of a lane
-  constexpr float kPeak = FORMAT == kQuantInt8 ? 127.f : 448.f;
-  extern __shared__ float2 smem_tab[];
-  __shared__ float s_gsum[8][D];
+  __shared__ float s_gsum[2][NG][D];  // raw group sums of a chunk, by turns
+  // rotations of a group's tokens (cosines, then sines, of H pairs at a time) and of a chunk's groups
+  extern __shared__ __align__(16) float s_token[];            // [kGroup][D]
+  float2* s_group = reinterpret_cast<float2*>(s_token + kGroup * D);  // [NG][n_lo]
+  __shared__ double s_omega[P];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv);
@@ -164,75 +260,65 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
   }
   const bool sums = chunk_sum != nullptr;
   const int n_lo = P - p.n_high;
-  const bool is_v = warp >= p.Ng;
-  const int w = is_v ? warp - p.Ng : warp;
+  const T* k_src = k_new + item * n_new * D + lane * E;
+  const T* v_src = v_new + item * n_new * D + lane * E;
+  T* k_tail = static_cast<T*>(qc.k_tail) + item * kGroup * D + lane * E;
+  T* v_tail = static_cast<T*>(qc.v_tail) + item * kGroup * D + lane * E;
 
   if (u_end > u0) {
-    const int64_t c_last = (u_end - 1) / p.Ng;
-    if (sums && u0 / p.Ng + blockIdx.y <= c_last) {
-      for (int i = threadIdx.x; i < summ::table_entries(p, D); i += blockDim.x)
-        smem_tab[i] = summ::table_entry(p, D, i);
+    const int64_t c_last = (u_end - 1) / NG;
+    if (sums && u0 / NG + blockIdx.y <= c_last) {
+      if (threadIdx.x < P)
+        s_omega[threadIdx.x] = static_cast<int>(threadIdx.x) < p.n_high ? 0.0 : summ::pair_omega(p, D, threadIdx.x);
+      __syncthreads();
+      for (int i = threadIdx.x; i < kGroup * P; i += 32 * NG) {
+        const int r = i / P, q = i % P;
+        const float2 t = q < p.n_high ? make_float2(1.f, 0.f) : summ::rotation(summ::token_offset(r), s_omega[q]);
+        float* to = s_token + r * D + q / H * (2 * H) + q % H;
+        to[0] = t.x;
+        to[H] = t.y;
+      }
+      for (int i = threadIdx.x; i < NG * n_lo; i += 32 * NG)
+        s_group[i] = summ::rotation(summ::group_offset(p, i / n_lo), s_omega[p.n_high + i % n_lo]);
       __syncthreads();
     }
-    const T* src = (is_v ? v_new : k_new) + item * n_new * D + lane * E;
-    const T* tail = static_cast<const T*>(is_v ? qc.v_tail : qc.k_tail) + item * kGroup * D + lane * E;
-    uint8_t* codes = is_v ? qc.v : qc.k;
-    float* scales = is_v ? qc.v_scale : qc.k_scale;
     // this lane's pairs: dims pair + j and pair + j + D/2
     const bool upper = lane >= 16;
     const int pair = (lane & 15) * E + (upper ? H : 0);
-    for (int64_t c = u0 / p.Ng + blockIdx.y; c <= c_last; c += gridDim.y) {
-      const int64_t u = c * p.Ng + w;
+    int turn = 0;
+    for (int64_t c = u0 / NG + blockIdx.y; c <= c_last; c += gridDim.y, turn ^= 1) {
+      const int64_t u = c * NG + warp;
       const bool in_table = u < qc.max_groups;  // the summary tables' capacity
       if (u >= u0 && u < u_end) {
         const int32_t slot = qc.table[item * qc.max_groups + (u - gone)];
-        Piece<T, E> x[kGroup];
-        uint32_t top = 0;
+        Piece<T, E> k[kGroup], v[kGroup];
+        const int64_t i0 = u * kGroup - p0;
+        if (i0 >= 0) {
+          const T *ks = k_src + i0 * D, *vs = v_src + i0 * D;
 #pragma unroll
-        for (int r = 0; r < kGroup; ++r) {
-          const int64_t i = u * kGroup + r - p0;
-          x[r].load(i >= 0 ? src + i * D : tail + r * D);
-        }
+          for (int r = 0; r < kGroup; ++r) k[r].load(ks + r * D);
 #pragma unroll
-        for (int r = 0; r < kGroup; ++r) top = max(top, x[r].top());
-        top = __reduce_max_sync(0xffffffffu, top);
-        const float amax = __uint_as_float(top);
-        const bool finite = top < 0x7f800000u;
-        const bool some = finite && amax >= 0x1p-100f;
-        const float inverse = some ? __fdiv_rn(kPeak, amax) : 0.f;
-        const float scale = some ? __fdiv_rn(amax, kPeak) : (finite ? 0.f : CUDART_NAN_F);
-        if (slot >= 0 && slot < qc.n_slots) {
-          uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * E;
+          for (int r = 0; r < kGroup; ++r) v[r].load(vs + r * D);
+        } else {  // the rows before the first new one are in the tail
 #pragma unroll
           for (int r = 0; r < kGroup; ++r) {
-            float y[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) y[i] = __fmul_rn(x[r].at(i), inverse);
-            store_codes(dst + r * D, finite ? quantise<FORMAT, E>(y) : 0u, std::integral_constant<int, E>());
+            k[r].load(i0 + r >= 0 ? k_src + (i0 + r) * D : k_tail + r * D);
+            v[r].load(i0 + r >= 0 ? v_src + (i0 + r) * D : v_tail + r * D);
           }
-          if (lane == 0) scales[slot] = scale;
-        } else if (lane == 0) {
-          flag_error(err, kErrPage);
         }
-        if (sums && !is_v) {
-          float gx[H], gy[H];
+        const bool held = slot >= 0 && slot < qc.n_slots;
+        if (!held && lane == 0) flag_error(err, kErrPage);
+        if (held) write_group<T, D, FORMAT>(k, qc.k, qc.k_scale, slot);
+        if (sums) {
+          RotatedSum<H> sum;
 #pragma unroll
-          for (int j = 0; j < H; ++j) gx[j] = gy[j] = 0.f;
-#pragma unroll
-          for (int r = 0; r < kGroup; ++r) {  // the batch builder's order and roundings
+          for (int r = 0; r < kGroup; ++r) {
             float px[H], py[H];
-            x[r].trade(upper, px, py);
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-              const int i = pair + j;
-              if (i < p.n_high) {
-                gx[j] = __fadd_rn(gx[j], px[j]);
-                gy[j] = __fadd_rn(gy[j], py[j]);
-              } else {
-                summ::add_rotated(gx[j], gy[j], px[j], py[j], smem_tab[r * n_lo + i - p.n_high]);
-              }
-            }
+            k[r].trade(upper, px, py);
+            sum.add(px, py, s_token + r * D + pair * 2);
           }
+          float gx[H], gy[H];
+          sum.get(gx, gy);
           if (in_table) {
             float* dst = group_sum + (item * qc.max_groups + u) * D;
 #pragma unroll
@@ -245,26 +331,26 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
           }
 #pragma unroll
           for (int j = 0; j < H; ++j) {
-            s_gsum[w][pair + j] = gx[j];
-            s_gsum[w][P + pair + j] = gy[j];
+            s_gsum[turn][warp][pair + j] = gx[j];
+            s_gsum[turn][warp][P + pair + j] = gy[j];
           }
         }
-      } else if (sums && !is_v && u < u0 && in_table) {  // a group an earlier call closed
+        if (held) write_group<T, D, FORMAT>(v, qc.v, qc.v_scale, slot);
+      } else if (sums && u < u0 && in_table) {  // a group an earlier call closed
         const float* row = group_sum + (item * qc.max_groups + u) * D;
-        for (int i = lane; i < D; i += 32) s_gsum[w][i] = __fmul_rn(row[i], static_cast<float>(kGroup));
+        for (int i = lane; i < D; i += 32) s_gsum[turn][warp][i] = __fmul_rn(row[i], static_cast<float>(kGroup));
       }
-      if (sums && !is_v && (c + 1) * p.Ng <= u_end) {  // the chunk closes: uniform over the K warps
-        k_barrier(p.Ng * 32);
+      if (sums && (c + 1) * NG <= u_end) {  // the chunk closes: uniform over the CTA
+        __syncthreads();  // the other turn's sums were last read before this
         if (c < p.n_chunks) {
           const float inv_c = 1.0f / p.C;
           float* dst = chunk_sum + (item * p.n_chunks + c) * D;
-          for (int i = threadIdx.x; i < P; i += p.Ng * 32) {
-            const float2 sc = summ::chunk_pair<D>(s_gsum, smem_tab + kGroup * n_lo, p.Ng, p.n_high, n_lo, i);
+          for (int i = threadIdx.x; i < P; i += 32 * NG) {
+            const float2 sc = summ::chunk_pair<D>(s_gsum[turn], s_group, NG, p.n_high, n_lo, i);
             dst[i] = __fmul_rn(sc.x, inv_c);
             dst[P + i] = __fmul_rn(sc.y, inv_c);
           }
         }
-        k_barrier(p.Ng * 32);
       }
     }
   }
@@ -274,39 +360,42 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
     __syncthreads();
     const int64_t t0 = max(p0, u_end * kGroup);
     const int rows = static_cast<int>(pb + 1 - t0);
-    const T* from = (is_v ? v_new : k_new) + (item * n_new + (t0 - p0)) * D;
-    T* to = static_cast<T*>(is_v ? qc.v_tail : qc.k_tail) + (item * kGroup + (t0 & 15)) * D;
-    for (int r = w; r < rows; r += p.Ng) {
-      Piece<T, E> x;
-      x.load(from + r * D + lane * E);
-      *reinterpret_cast<Piece<T, E>*>(to + r * D + lane * E) = x;
+    for (int r = warp; r < rows; r += NG) {
+      Piece<T, E> k, v;
+      k.load(k_src + (t0 - p0 + r) * D);
+      v.load(v_src + (t0 - p0 + r) * D);
+      *reinterpret_cast<Piece<T, E>*>(k_tail + ((t0 & 15) + r) * D) = k;
+      *reinterpret_cast<Piece<T, E>*>(v_tail + ((t0 & 15) + r) * D) = v;
     }
   }
   pdl_trigger();
 }
 
-template <typename T, int D, int FORMAT>
+template <typename T, int D, int FORMAT, int NG>
 cudaError_t launch_t(const LayerParams& p, const QuantCache& qc, const void* k_new,
                      const void* v_new, int n_new, const int32_t* counts, const int64_t* pos,
                      float* chunk_sum, float* group_sum, unsigned* err, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
-  // a call's new rows touch at most this many chunks; ~8 CTAs per SM, each looping
-  const int64_t chunks = (n_new + p.C - 2) / p.C + 1;
-  int64_t gy = (device_sm_count() * 8LL + items - 1) / items;
+  // A call's new rows touch at most this many chunks.  With summaries the CTAs that
+  // fit at a time loop over them, so that each builds its rotations once; without, a
+  // CTA takes one chunk, which evens out ragged batches (61 us for a 64K prompt,
+  // four chunks a CTA 63 us).
+  const int64_t chunks = (static_cast<int64_t>(n_new) + p.C - 2) / p.C + 1;
+  int64_t gy = chunk_sum ? static_cast<int64_t>(device_sm_count()) * ctas_per_sm(NG) / items : std::min<int64_t>(chunks, 65535);
   gy = gy < 1 ? 1 : (gy > chunks ? chunks : gy);
-  const size_t smem = chunk_sum ? summ::table_entries(p, D) * sizeof(float2) : 0;
-  return launch_pdl(quant_append_kernel<T, D, FORMAT>, dim3(static_cast<unsigned>(items), static_cast<unsigned>(gy)),
-                    dim3(64 * p.Ng), smem, s, 1, p, qc, static_cast<const T*>(k_new),
+  const size_t smem = chunk_sum ? kGroup * D * sizeof(float) + NG * (D / 2 - p.n_high) * sizeof(float2) : 0;
+  return launch_pdl(quant_append_kernel<T, D, FORMAT, NG>, dim3(static_cast<unsigned>(items), static_cast<unsigned>(gy)),
+                    dim3(32 * NG), smem, s, 1, p, qc, static_cast<const T*>(k_new),
                     static_cast<const T*>(v_new), n_new, counts, pos, chunk_sum, group_sum, err);
 }
 
 template <typename T, int D>
-cudaError_t launch_f(const LayerParams& p, const QuantCache& qc, const void* k_new,
-                     const void* v_new, int n_new, const int32_t* counts, const int64_t* pos,
-                     float* chunk_sum, float* group_sum, unsigned* err, cudaStream_t s) {
-  return qc.format == kQuantInt8
-             ? launch_t<T, D, kQuantInt8>(p, qc, k_new, v_new, n_new, counts, pos, chunk_sum, group_sum, err, s)
-             : launch_t<T, D, kQuantE4m3>(p, qc, k_new, v_new, n_new, counts, pos, chunk_sum, group_sum, err, s);
+cudaError_t launch_f(const LayerParams& p, const QuantCache& qc, const void* k, const void* v, int n,
+                     const int32_t* counts, const int64_t* pos, float* cs, float* gs, unsigned* err,
+                     cudaStream_t s) {
+  auto* kernel = qc.format == kQuantInt8 ? launch_t<T, D, kQuantInt8, 4> : launch_t<T, D, kQuantE4m3, 4>;
+  if (p.Ng == 8) kernel = qc.format == kQuantInt8 ? launch_t<T, D, kQuantInt8, 8> : launch_t<T, D, kQuantE4m3, 8>;
+  return kernel(p, qc, k, v, n, counts, pos, cs, gs, err, s);
 }
 
 }  // namespace

@@ -31,16 +31,24 @@ __host__ __device__ inline int table_entries(const LayerParams& p, int D) {
 // Entry idx of the table.  The angle is formed in double from
 // omega_i = theta^(-2i/D) and the exact half-integer offset, then rounded once
 // to float for sincosf.
+__device__ inline double pair_omega(const LayerParams& p, int D, int i) {
+  return pow(p.theta, -2.0 * i / D);
+}
+__device__ inline float2 rotation(double off, double omega) {
+  float s, c;
+  sincosf(static_cast<float>(off * omega), &s, &c);
+  return make_float2(c, s);
+}
+// Offset of a group's token o, and of group w of a chunk, to the span's centre.
+__device__ inline double token_offset(int o) { return 0.5 * (kGroup - 1) - o; }
+__device__ inline double group_offset(const LayerParams& p, int w) { return 0.5 * (p.C - kGroup) - w * kGroup; }
+
 __device__ inline float2 table_entry(const LayerParams& p, int D, int idx) {
   const int n_lo = D / 2 - p.n_high;
   const bool is_g = idx < kGroup * n_lo;
   const int j = is_g ? idx : idx - kGroup * n_lo;
   const int o = j / n_lo;
-  const double omega = pow(p.theta, -2.0 * (p.n_high + j % n_lo) / D);
-  const double off = is_g ? 0.5 * (kGroup - 1) - o : 0.5 * (p.C - kGroup) - o * kGroup;
-  float s, c;
-  sincosf(static_cast<float>(off * omega), &s, &c);
-  return make_float2(c, s);
+  return rotation(is_g ? token_offset(o) : group_offset(p, o), pair_omega(p, D, p.n_high + j % n_lo));
 }
 
 // Adds the (x, y) pair of dims (i, i + D/2) rotated by r = (cos, sin) to (sx, sy).

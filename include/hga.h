@@ -585,8 +585,8 @@ hga_status hga_decode_step_paged(const hga_config* cfg, const void* q, const int
  * or NaN gets codes 0 and a NaN scale.
  * With chunk_sum and group_sum (both or neither), the summary rows of the closed
  * groups, and of the chunks that end with one, are written as
- * hga_build_summaries writes them, bit for bit, provided the rows of the
- * chunk's earlier groups stand in group_sum; then n_alloc is max_groups * 16,
+ * hga_build_summaries writes them, bit for bit (finite rows), provided the rows
+ * of the chunk's earlier groups stand in group_sum; then n_alloc is max_groups * 16,
  * max_groups a multiple of C / 16, and a group whose index is max_groups or more
  * is flagged.
  *   k_new, v_new  device [B, Hkv, n_new, D] of cfg->dtype (keys post-RoPE)
