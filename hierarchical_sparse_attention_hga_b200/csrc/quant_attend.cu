@@ -53,7 +53,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 2;             // units a warp works on at a time
 constexpr int kStages = 2;           // tiles in a warp's ring
 static_assert(32 % kTile == 0, "a tile's slots come from one block of 32");
-constexpr int kItemCost = 4;         // an item's fixed work, in units (see the slices)
+constexpr int kItemCost = 8;         // an item's fixed work, in units (see the slices)
 constexpr int kMinSlice = 2;         // units a warp takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -230,21 +230,30 @@ struct Warp {
   float o[NK][NT][4];
   float ref_w[NT][2], ref_s[NT][2], l[NT][2];
 
+  using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
+
   // Query heads of (b, h): column n of tile nt is head nt * 8 + n; with GM == 4
   // columns 4..7 repeat heads 0..3.
-  __device__ __forceinline__ void load_q(const T* q, const LayerParams& p, int b, int h) {
+  __device__ __forceinline__ void fetch_q(const T* q, const LayerParams& p, int b, int h, Row (&raw)[NT][NK]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int head = GM == 4 ? g & 3 : nt * 8 + g;
+      const T* row = q + (static_cast<int64_t>(b) * p.Hq + h * p.G + head) * D + c * 16;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks)
+        raw[nt][ks] = head < p.G ? __ldg(reinterpret_cast<const Row*>(row + (ks >> 2) * 64 + (ks & 3) * 4)) : Row{};
+    }
+  }
+  __device__ __forceinline__ void load_q(const Row (&raw)[NT][NK]) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float x[NK][4];
       uint32_t top = 0;
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
-        if (head < p.G)
-          load4(q + (static_cast<int64_t>(b) * p.Hq + h * p.G + head) * D + (ks >> 2) * 64 + c * 16 + (ks & 3) * 4, x[ks]);
-        else
-          x[ks][0] = x[ks][1] = x[ks][2] = x[ks][3] = 0.f;
+        unpack(raw[nt][ks], x[ks]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, finite_bits(x[ks][i]));
       }
@@ -376,7 +385,6 @@ struct Warp {
   // Tail rows (rest of them valid) as one unit.  All loads come first.
   __device__ void tail(const T* kt, const T* vt, int rest, float2* group, int stride, int unit, int G) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
     Row kr[2][NK], vr[4][D / 32];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -522,8 +530,11 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
     for (int k = 0; k < kStages; ++k) ptx::mbar_init(&s_full[warp][k], 1);
     ptx::fence_barrier_init();
+    ptx::prefetch_tensormap(&map_k);
+    ptx::prefetch_tensormap(&map_v);
   }
-  pdl_wait();
+  // Positions are never written by this library; the counts of evicted groups are.
+  if (qc.evicted) pdl_wait();
 
   auto worker = [&]() { return static_cast<int64_t>(blockIdx.x) * kWarps + warp; };
   auto slice_length = [&](int64_t all) {
@@ -573,7 +584,10 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   {
     const int64_t all = s_all, slice = slice_length(all);
     const int64_t lo = slice * worker();
-    if (lo >= all) return;
+    if (lo >= all) {
+      pdl_wait();  // a grid ends after the one before it, even if it has no work
+      return;
+    }
     left = static_cast<int>(min(slice, all - lo));
     int owner = -1;  // the last thread whose items begin at or before lo
 #pragma unroll
@@ -599,6 +613,8 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     skip = static_cast<int>(lo - start);
   }
 
+  if (!qc.evicted) pdl_wait();
+  pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
   W w;
   int stage = 0;       // of the ring, and its phase
   uint32_t phase = 0;
@@ -691,9 +707,11 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     };
 
     int u = u_lo;
+    typename W::Row q_raw[NT][NK];
+    w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
 #pragma unroll
     for (int k = 0; k < kStages; ++k) issue((stage + k) % kStages);
-    w.load_q(q, p, b, h);
+    w.load_q(q_raw);
     w.clear();
     if (u_hi > un.groups) {
       const int64_t at = static_cast<int64_t>(item) * kQuantGroup * D;
@@ -813,7 +831,6 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
               make_float4(w.ref_w[nt][e], w.ref_s[nt][e], w.l[nt][e], 0.f);
       }
   }
-  pdl_trigger();
 }
 
 // Merges an item's partials.  The first blocks along y: outputs and LSE of
@@ -830,55 +847,81 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
   constexpr int kMergeWarps = merge_warps(SPLIT), kMergeThreads = kMergeWarps * 32;
   constexpr int kHeads = kMergeWarps / SPLIT;
   __shared__ float s_sum[SPLIT > 1 ? kMergeWarps : 1][D];
-  __shared__ float s_l[kMergeWarps];
+  __shared__ float4 s_warp[SPLIT > 1 ? kMergeWarps : 1];
   __shared__ float s_ref[16][2];
   __shared__ float s_add[kMergeEntries];
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv), h = static_cast<int>(item % p.Hkv);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t pb = pos[b];
   pdl_wait();
-  const QuantItem it = quant_item(qc, pos[b], item, nullptr);
+  pdl_trigger();
+  const int2 found = ws.parts[item];  // written if the item has units
+  const QuantItem it = quant_item(qc, pb, item, nullptr);
   const int units = it.units();
-  const int2 parts = units ? ws.parts[item] : make_int2(0, 0);
+  const int2 parts = units ? found : make_int2(0, 0);
   const int64_t first = parts.x + item;
   const float4* stat = reinterpret_cast<const float4*>(ws.stat) + first * 16;
   const int head_blocks = (p.G + kHeads - 1) / kHeads;
   if (static_cast<int>(blockIdx.y) < head_blocks) {
     const int head = blockIdx.y * kHeads + warp / SPLIT, share = warp % SPLIT;
     const bool on = head < p.G;
-    float rw = kNoRef, rs = kNoRef;
-    if (on)
-      for (int i = lane; i < parts.y; i += 32) {
-        const float4 s = stat[i * 16 + head];
-        rw = fmaxf(rw, s.x);
-        rs = fmaxf(rs, s.y);
-      }
-    rw = warp_max(rw);
-    rs = warp_max(rs);
-    float acc[D / 32], l = 0.f;
+    float rw = kNoRef, rs = kNoRef, acc[D / 32], l = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
-    if (on) {
-#pragma unroll 4
-      for (int i = share; i < parts.y; i += SPLIT) {
-        const float4 s = stat[i * 16 + head];
-        const float* row = ws.sum + ((first + i) * p.G + head) * D;
-        const float f = ex2(s.x - rw);
-        l += s.z * ex2(s.y - rs);
+    const float* rows = ws.sum + (first * p.G + head) * D + lane;
+    const int count = on ? parts.y : 0;
+    constexpr int kBatch = 4;  // partials on their way at a time
+    for (int i0 = share; i0 < count; i0 += SPLIT * kBatch) {
+      float4 s[kBatch];
+      float x[kBatch][D / 32];
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] += f * row[j * 32 + lane];
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * SPLIT;
+        s[k] = make_float4(kNoRef, kNoRef, 0.f, 0.f);
+        if (i < count) s[k] = stat[i * 16 + head];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[k][j] = i < count ? rows[static_cast<int64_t>(i) * p.G * D + j * 32] : 0.f;
       }
+      float nw = rw, ns = rs;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        nw = fmaxf(nw, s[k].x);
+        ns = fmaxf(ns, s[k].y);
+      }
+      const float fw = ex2(rw - nw);
+      l *= ex2(rs - ns);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] *= fw;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = ex2(s[k].x - nw);
+        l += s[k].z * ex2(s[k].y - ns);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[j] += f * x[k][j];
+      }
+      rw = nw;
+      rs = ns;
     }
-    if constexpr (SPLIT > 1) {
+    if constexpr (SPLIT > 1) {  // one head a block: its warps' sums
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) s_sum[warp][j * 32 + lane] = acc[j];
-      if (lane == 0) s_l[warp] = l;
+      if (lane == 0) s_warp[warp] = make_float4(rw, rs, l, 0.f);
       __syncthreads();
       if (share == 0) {
-        for (int k = 1; k < SPLIT; ++k) {
-          l += s_l[warp + k];
+        const float4 s = s_warp[lane];
+        static_assert(SPLIT == 32, "a lane for every warp");
+        rw = warp_max(s.x);
+        rs = warp_max(s.y);
+        l = warp_sum(s.z * ex2(s.y - rs));
+        const float f = ex2(s.x - rw);
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) acc[j] += s_sum[warp + k][j * 32 + lane];
+        for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < SPLIT; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) acc[j] += fk * s_sum[k][j * 32 + lane];
         }
       }
     }
@@ -909,7 +952,7 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
         }
       }
       __syncthreads();
-      const Units un = units_of(p, it, pos[b], group_idx != nullptr);
+      const Units un = units_of(p, it, pb, group_idx != nullptr);
       const int stride = qc.max_groups + p.kg;
       auto unit_weight = [&](int u) {
         float sum = 0.f;
@@ -941,7 +984,6 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
       }
     }
   }
-  pdl_trigger();
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
