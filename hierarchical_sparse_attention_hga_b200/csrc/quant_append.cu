@@ -245,6 +245,7 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv);
   pdl_wait();
+  pdl_trigger();  // dependents wait for the whole grid; they may be launched as its CTAs leave
 
   const int64_t pb = pos[b];
   const int64_t count = counts ? counts[b] : n_new;
@@ -368,7 +369,6 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
       *reinterpret_cast<Piece<T, E>*>(v_tail + ((t0 & 15) + r) * D) = v;
     }
   }
-  pdl_trigger();
 }
 
 template <typename T, int D, int FORMAT, int NG>

@@ -533,8 +533,11 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     ptx::prefetch_tensormap(&map_k);
     ptx::prefetch_tensormap(&map_v);
   }
-  // Positions are never written by this library; the counts of evicted groups are.
-  if (qc.evicted) pdl_wait();
+  // What kernels of this library write is read, and the scratch that the merge of
+  // an earlier call may still read is written, behind pdl_wait: the counts of
+  // evicted groups first of all.  Positions and queries come before it.
+  bool waited = qc.evicted != nullptr;
+  if (waited) pdl_wait();
 
   auto worker = [&]() { return static_cast<int64_t>(blockIdx.x) * kWarps + warp; };
   auto slice_length = [&](int64_t all) {
@@ -585,7 +588,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int64_t all = s_all, slice = slice_length(all);
     const int64_t lo = slice * worker();
     if (lo >= all) {
-      pdl_wait();  // a grid ends after the one before it, even if it has no work
+      if (!waited) pdl_wait();  // a grid ends after the one before it, even if it has no work
       return;
     }
     left = static_cast<int>(min(slice, all - lo));
@@ -613,8 +616,6 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     skip = static_cast<int>(lo - start);
   }
 
-  if (!qc.evicted) pdl_wait();
-  pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
   W w;
   int stage = 0;       // of the ring, and its phase
   uint32_t phase = 0;
@@ -630,6 +631,13 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (u_hi <= 0) break;  // only the item's fixed part
     left -= un.total + kItemCost - skip;
     skip = 0;
+    typename W::Row q_raw[NT][NK];
+    w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
+    if (!waited) {
+      pdl_wait();
+      waited = true;
+    }
+    pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
     if (lane == 0 && u_lo == 0) {  // this warp has the item's first unit; its last one is total - u_hi further on
       const int64_t slice = slice_length(s_all);
       ws.parts[item] = make_int2(static_cast<int>(worker()), static_cast<int>((max(0, -left) + slice - 1) / slice) + 1);
@@ -707,8 +715,6 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     };
 
     int u = u_lo;
-    typename W::Row q_raw[NT][NK];
-    w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
 #pragma unroll
     for (int k = 0; k < kStages; ++k) issue((stage + k) % kStages);
     w.load_q(q_raw);

@@ -90,6 +90,7 @@ quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* __restrict__ pos, int 
   const int32_t* t_in = qc.table + item * max_groups;
   int32_t* t_out = table_out + item * max_groups;
   pdl_wait();
+  pdl_trigger();  // dependents wait for the whole grid; they may be launched as its CTAs leave
 
   for (int i = tid; i < max_groups; i += NT) {
     s_weight[i] = __float_as_uint(w_in[i]);
@@ -211,7 +212,6 @@ quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* __restrict__ pos, int 
   }
   write_table();
   if (tid == 0) evicted_out[item] = gone + (n - kept_n);
-  pdl_trigger();
 }
 
 template <int NT, int ROWS>
