@@ -915,8 +915,8 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
       if (lane == 0) s_warp[warp] = make_float4(rw, rs, l, 0.f);
       __syncthreads();
       if (share == 0) {
-        const float4 s = s_warp[lane];
-        static_assert(SPLIT == 32, "a lane for every warp");
+        static_assert(SPLIT <= 32, "a lane for every warp");
+        const float4 s = lane < SPLIT ? s_warp[lane] : make_float4(kNoRef, kNoRef, 0.f, 0.f);
         rw = warp_max(s.x);
         rs = warp_max(s.y);
         l = warp_sum(s.z * ex2(s.y - rs));
@@ -1068,14 +1068,18 @@ cudaError_t launch_merge_split(const LayerParams& p, const QuantCache& qc, const
                     static_cast<TO*>(out), lse);
 }
 
-// Few items have many partials each: a block per head; many items: a warp per head.
+// Warps that share a head's partials, by how many partials an item has if all are
+// alike: with 14 each (128 items, weights) 8 warps take 12 us and 32 warps, whose
+// blocks need three waves, 19; with 7 each (256 items) one warp is 3 us faster than 8.
 template <int D, typename TO>
 cudaError_t launch_merge(const LayerParams& p, const QuantCache& qc, const int64_t* pos,
                          const Workspace& ws, const int32_t* gi, const float* wi, float* wo, void* out,
                          float* lse, cudaStream_t s) {
-  return p.B * p.Hkv < device_sm_count()
-             ? launch_merge_split<D, TO, 32>(p, qc, pos, ws, gi, wi, wo, out, lse, s)
-             : launch_merge_split<D, TO, 1>(p, qc, pos, ws, gi, wi, wo, out, lse, s);
+  const int64_t each = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(heads_rounded(p)) * kWarps / (static_cast<int64_t>(p.B) * p.Hkv);
+  auto* kernel = launch_merge_split<D, TO, 1>;
+  if (each >= 8) kernel = launch_merge_split<D, TO, 8>;
+  if (each >= 64) kernel = launch_merge_split<D, TO, 32>;
+  return kernel(p, qc, pos, ws, gi, wi, wo, out, lse, s);
 }
 
 }  // namespace
