@@ -85,14 +85,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// 4 bytes from global to shared memory; zero when !valid (nothing is read).
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
@@ -517,13 +509,14 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   extern __shared__ uint8_t s_dyn[];                    // [kWarps][kRing], then [kWarps][kg] routed ids
   uint8_t* s_rings = s_dyn + (1024 - ptx::smem_u32(s_dyn) % 1024) % 1024;
   __shared__ uint64_t s_full[kWarps][kStages];
-  __shared__ float s_scale[kWarps][kStages][kTile][2];  // k_scale, v_scale
-  __shared__ int s_state[kWarps][kStages][kTile];       // 1: in the ring, 0: no tokens, -1: id not kept
+  // per unit, two blocks of 32: k_scale, v_scale as mantissa and exponent, state (1: in
+  // the ring, 0: no tokens, -1: id not kept)
+  __shared__ float4 s_units[kWarps][2][32];
   __shared__ int64_t s_before[kThreads];                // list length before each thread's items
   __shared__ int64_t s_all;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   uint8_t* ring = s_rings + warp * kRing;
-  const uint32_t ring_at = ptx::smem_u32(ring), scale_at = ptx::smem_u32(&s_scale[warp][0][0][0]);
+  const uint32_t ring_at = ptx::smem_u32(ring);
   int* routed = reinterpret_cast<int*>(s_rings + kWarps * kRing) + warp * p.kg;
   const int items = p.B * p.Hkv;
   if (lane == 0) {
@@ -686,32 +679,41 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       flag_error(err, kErrPage);
       return -1;
     };
+    // The scales of a block's units, a lane each, are on their way from its first
+    // copies to the tile behind them, and then in shared memory.
+    int slots = 0, slots_next = load_slots(u_lo), issued = 0, staged = -1;
+    float k_scale = 0.f, v_scale = 0.f;
+    auto stage_scales = [&]() {
+      if (staged >= 0) {
+        float mant, ex;
+        split_scale(v_scale, mant, ex);
+        s_units[warp][(staged >> 5) & 1][lane] = make_float4(k_scale, mant, ex, slots >= 0 ? 1.f : static_cast<float>(slots + 1));
+        staged = -1;
+      }
+    };
     // starts the copies of the slice's next tile, if there is one left
-    int slots = 0, slots_next = load_slots(u_lo), issued = 0;
     auto issue = [&](int stage) {
       if (u_lo + issued < g_hi) {
         if ((issued & 31) == 0) {
           slots = checked(slots_next, u_lo + issued);
           slots_next = load_slots(u_lo + issued + 32);
+          k_scale = slots >= 0 ? qc.k_scale[slots] : 0.f;
+          v_scale = slots >= 0 ? qc.v_scale[slots] : 0.f;
+          staged = issued;
         }
         uint8_t* dst = ring + stage * kTile * kUnitBytes;
         if (lane == 0) ptx::mbar_expect_tx(&s_full[warp][stage], kTile * kUnitBytes);
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
           const int slot = __shfl_sync(0xffffffffu, slots, (issued & 31) + j);
-          const bool valid = slot >= 0;
-          if (lane < 2)
-            copy4(scale_at + ((stage * kTile + j) * 2 + lane) * 4, (lane ? qc.v_scale : qc.k_scale) + (valid ? slot : 0), valid);
           if (lane == 0) {  // a row before the first reads as zeros
-            const int row = valid ? slot * kQuantGroup : -kQuantGroup;
+            const int row = slot >= 0 ? slot * kQuantGroup : -kQuantGroup;
             ptx::tma_load_2d(dst + j * kUnitBytes, &map_k, &s_full[warp][stage], 0, row);
             ptx::tma_load_2d(dst + j * kUnitBytes + kUnitBytes / 2, &map_v, &s_full[warp][stage], 0, row);
-            s_state[warp][stage][j] = valid ? 1 : slot + 1;
           }
         }
         issued += kTile;
       }
-      copy_commit();
     };
 
     int u = u_lo;
@@ -724,8 +726,9 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
              stride, un.groups, p.G);
     }
+    stage_scales();
+    __syncwarp();
     for (; u < g_hi; u += kTile) {
-      copy_wait<kStages - 1>();
       // after a wait gave up, the others are short; every copy is still waited for
       if (!__all_sync(0xffffffffu, ptx::mbar_wait_ns(&s_full[warp][stage], phase, kWaitLimit, alive ? 50000000ull : 1000000ull))) {
         alive = false;
@@ -756,16 +759,17 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             if constexpr (W::kSplitQ) mma(x[j][nt], a0, a1, a2, a3, w.ql[nt][ks][0], w.ql[nt][ks][1]);
           }
         }
-        const float k_scale = s_scale[warp][stage][j][0];
-        const int state = s_state[warp][stage][j];
+        const int r = u - u_lo + j;
+        const float4 unit = s_units[warp][(r >> 5) & 1][r & 31];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[j][nt][i] = state > 0 ? x[j][nt][i] * (w.f[nt][i & 1] * k_scale) : -CUDART_INF_F;
-        split_scale(s_scale[warp][stage][j][1], mant[j], ex[j]);
+            x[j][nt][i] = unit.w > 0.f ? x[j][nt][i] * (w.f[nt][i & 1] * unit.x) : -CUDART_INF_F;
+        mant[j] = unit.y;
+        ex[j] = unit.z;
         at[j] = u + j < g_hi ? u + j : -1;
-        kept[j] = state >= 0;
+        kept[j] = unit.w >= 0.f;
       }
       uint32_t pb[kTile][NT][2][2];
       w.template softmax<kTile>(x, mant, ex, pb, group, stride, at, kept, p.G);
@@ -804,7 +808,8 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             for (int e = 0; e < 4; ++e) w.o[2 * i + half][nt][e] += s[e];
           }
       }
-      __syncwarp();  // every lane has read the stage
+      stage_scales();
+      __syncwarp();  // every lane has read the stage, and written its scales
       issue(stage);
       if (++stage == kStages) {
         stage = 0;
