@@ -247,14 +247,14 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
   pdl_wait();
   pdl_trigger();  // dependents wait for the whole grid; they may be launched as its CTAs leave
 
-  const int64_t pb = pos[b];
+  const int64_t pb = min(max(pos[b], int64_t{-2}), kQuantMaxPos + 1);  // out of range stays so
   const int64_t count = counts ? counts[b] : n_new;
   const int64_t p0 = pb - count + 1;  // position of the first new row
   const int64_t gone = qc.evicted ? qc.evicted[item] : 0;
   const int64_t u0 = p0 >> 4, u_end = (pb + 1) >> 4;  // groups [u0, u_end) close
   const int64_t open = (pb + 1) & 15 ? 1 : 0;
   if (count == 0) return;
-  if (count < 0 || count > n_new || p0 < 0 || gone < 0 || u0 < gone ||
+  if (pb > kQuantMaxPos || count < 0 || count > n_new || p0 < 0 || gone < 0 || u0 < gone ||
       u_end + open - gone > qc.max_groups) {
     if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(err, kErrPos);
     return;

@@ -1026,7 +1026,7 @@ cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void
   // at most the resident CTAs, and no more than the largest possible list has slices
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
   int64_t most = qc.max_groups;
-  if (group_idx) most = std::min(most, static_cast<int64_t>(p.sink + p.local + 1) * p.Ng) + p.kg + 1;
+  if (group_idx) most = std::min(most, (static_cast<int64_t>(p.sink) + p.local + 1) * p.Ng) + p.kg + 1;
   const int64_t slices = (items * (most + kItemCost) + kMinSlice - 1) / kMinSlice;
   const int64_t resident = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(GM);
   const unsigned grid = static_cast<unsigned>(std::min((slices + kWarps - 1) / kWarps, resident));

@@ -16,6 +16,7 @@ namespace hga {
 
 constexpr int kQuantGroup = 16;  // tokens per group (cfg group is 16)
 constexpr int kQuantMaxGroups = 1 << 20;  // table entries per (sequence, KV head)
+constexpr int64_t kQuantMaxPos = int64_t{1} << 40;  // positions count evicted tokens too
 constexpr int64_t kQuantMaxSlots = (1 << 27) - 1;  // a slot's first row is an int32 coordinate
 
 struct QuantCache {
@@ -48,10 +49,15 @@ __device__ __forceinline__ QuantItem quant_item(const QuantCache& qc, int64_t po
                                                 unsigned* err) {
   QuantItem it{0, 0, true};
   if (pos == -1) return it;
+  if (pos < -1 || pos > kQuantMaxPos) {
+    flag_error(err, kErrPos);
+    it.ok = false;
+    return it;
+  }
   const int64_t gone = qc.evicted ? qc.evicted[item] : 0;
   const int64_t closed = ((pos + 1) >> 4) - gone;
   const int rest = static_cast<int>((pos + 1) & 15);
-  if (pos < -1 || gone < 0 || closed < 0 || closed + (rest > 0) > qc.max_groups) {
+  if (gone < 0 || closed < 0 || closed + (rest > 0) > qc.max_groups) {
     flag_error(err, kErrPos);
     it.ok = false;
     return it;

@@ -253,7 +253,7 @@ def test_append_flags_what_does_not_fit():
     c = Cache(3, 2, 128, 4, seed=4, evicts=True)
     good = c.k.clone()
     new = c.rng.standard_normal((3, 2, 20, 128))
-    for pos, counts, gone in (([18, 19, 19], None, 0), ([-1, 19, 19], None, 0), ([64, 19, 19], None, 0),
+    for pos, counts, gone in (([18, 19, 19], None, 0), ([-1, 19, 19], None, 0), ([64, 19, 19], None, 0), ([2 ** 63 - 1, 19, 19], None, 0), ([-2 ** 63, 19, 19], None, 0),
                               ([19, 19, 19], [21, 20, 20], 0), ([19, 19, 19], [-1, 20, 20], 0),
                               ([19, 19, 19], None, 1), ([19, 19, 19], None, -1)):
         c.k.copy_(good)
@@ -416,7 +416,7 @@ def test_attend_flags_positions_and_slots():
     q = c.q()
     right = c.attend(q)
     saved = c.pos.copy()
-    for bad in (-2, 160, 1 << 40):
+    for bad in (-2, 160, 1 << 40, 2 ** 63 - 1, -2 ** 63):
         c.pos = saved.copy()
         c.pos[1] = bad
         out, lse = c.attend(q)
@@ -443,6 +443,50 @@ def test_attend_a_long_sequence_and_a_pool_past_4_gib():
     w_in = torch.zeros(1, 1, groups, device="cuda")
     w_out = torch.full_like(w_in, -5)
     c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+
+
+@pytest.mark.parametrize("batch,heads_kv,shared,longest", [(300, 8, 2, 60), (1100, 2, 1, 40), (3, 3, 4, 16)])
+def test_attend_many_items_and_one_group(batch, heads_kv, shared, longest):
+    """More (sequence, KV head) items than warps on the card, and tables of a single entry."""
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, longest + 1, batch)]
+    c = Cache(batch, heads_kv, 64, -(-longest // 16), heads_q=shared * heads_kv, seed=21)
+    c.fill(lens)
+    q = c.q()
+    w_in = torch.rand(batch, heads_kv, c.max, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_attend_a_pool_that_others_filled(fmt):
+    """Every finite code (int8 -128 among them), scales of any sign and size, zero and
+    subnormal ones; no LSE asked for."""
+    c = Cache(2, 2, 128, 20, fmt=fmt, heads_q=6, seed=22)
+    values = Q.code_values(fmt)
+    fine = np.flatnonzero(np.isfinite(values))
+    c.pos[:] = [16 * 20 - 1, 16 * 7 - 1]
+    table = c.table.cpu().numpy()
+    for codes, scales, name, size in ((c.k, c.ks, "k", 0.02), (c.v, c.vs, "v", 1.0)):
+        pool = c.rng.choice(fine, codes.shape).astype(np.uint8)
+        sc = (size / 100 * np.exp(c.rng.standard_normal(c.n_slots)) * c.rng.choice([1, 1, 1, -1], c.n_slots)).astype(np.float32)
+        sc[table[0, 0, 3]] = 0
+        if name == "v":
+            sc[table[0, 1, 4]] = 1e-40
+            sc[table[1, 0, 2]] = 1e30
+        codes.copy_(torch.tensor(pool))
+        scales.copy_(torch.tensor(sc))
+        for b, n in enumerate((20, 7)):
+            for h in range(2):
+                getattr(c.items[b][h], name).extend((values[pool[s]], sc[s]) for s in table[b, h, :n])
+    q = c.q()
+    got = c.attend(q)
+    c.check_attend(q, got)
+    out = torch.empty_like(got[0])
+    need = B.hga_quant_attend_workspace_size(c.layer, c.max)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    B.hga_quant_attend(c.layer, c.view(), to_gpu(q, "bf16"), c.pos_t(), out, workspace=ws, workspace_bytes=need)
+    assert torch.equal(out, got[0])
 
 
 # ---- evict
