@@ -44,34 +44,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two floats in one register pair; each half of an operation is rounded as the
-// scalar one.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Sums of H rotated pairs over a group's rows, with the batch builder's roundings
 // (summ::add_rotated): x += x c - y s, y += x s + y c.  High-frequency pairs have
 // (c, s) = (1, 0), which leaves the bits of finite rows as a plain sum has them.
@@ -81,12 +53,12 @@ template <> struct RotatedSum<2> {
   uint64_t x = 0, y = 0;
   __device__ __forceinline__ void add(const float (&a)[2], const float (&b)[2], const float* table) {
     const float4 t = *reinterpret_cast<const float4*>(table);
-    const uint64_t c = pack2(t.x, t.y), s = pack2(t.z, t.w), a2 = pack2(a[0], a[1]), b2 = pack2(b[0], b[1]);
-    x = add2(x, fma2(a2, c, mul2(b2, s ^ 0x8000000080000000ull)));
-    y = add2(y, fma2(a2, s, mul2(b2, c)));
+    const uint64_t c = f32x2::pack(t.x, t.y), s = f32x2::pack(t.z, t.w), a2 = f32x2::pack(a[0], a[1]), b2 = f32x2::pack(b[0], b[1]);
+    x = f32x2::add(x, f32x2::fma(a2, c, f32x2::mul(b2, s ^ 0x8000000080000000ull)));
+    y = f32x2::add(y, f32x2::fma(a2, s, f32x2::mul(b2, c)));
   }
   __device__ __forceinline__ void get(float (&a)[2], float (&b)[2]) const {
-    const float2 u = unpack2(x), v = unpack2(y);
+    const float2 u = f32x2::unpack(x), v = f32x2::unpack(y);
     a[0] = u.x; a[1] = u.y; b[0] = v.x; b[1] = v.y;
   }
 };
@@ -213,14 +185,14 @@ __device__ __forceinline__ void write_group(const Piece<T, D / 32> (&x)[kGroup],
   const bool some = finite && amax >= 0x1p-100f;
   const float inverse = some ? __fdiv_rn(kPeak, amax) : 0.f;
   const float scale = some ? __fdiv_rn(amax, kPeak) : (finite ? 0.f : CUDART_NAN_F);
-  const uint64_t inverse2 = pack2(inverse, inverse);
+  const uint64_t inverse2 = f32x2::pack(inverse, inverse);
   uint8_t* dst = codes + static_cast<int64_t>(slot) * kGroup * D + lane * E;
 #pragma unroll
   for (int r = 0; r < kGroup; ++r) {
     float y[E];
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
-      const float2 t = unpack2(mul2(pack2(x[r].at(i), x[r].at(i + 1)), inverse2));
+      const float2 t = f32x2::unpack(f32x2::mul(f32x2::pack(x[r].at(i), x[r].at(i + 1)), inverse2));
       y[i] = t.x;
       y[i + 1] = t.y;
     }

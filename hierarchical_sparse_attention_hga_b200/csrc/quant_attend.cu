@@ -71,11 +71,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  const float2 v = f32x2::unpack(x);
+  return f32x2::pack(ex2(v.x), ex2(v.y));
+}
+
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                     uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero accumulators.
+__device__ __forceinline__ void mma_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transposes an 8 x 8 matrix of halves held two per lane.
@@ -219,8 +232,9 @@ struct Warp {
 
   uint32_t qh[NT][NK][2], ql[kSplitQ ? NT : 1][kSplitQ ? NK : 1][2];
   float f[NT][2];                                      // score scale of this lane's columns (log2 units)
-  float o[NK][NT][4];
-  float ref_w[NT][2], ref_s[NT][2], l[NT][2];
+  uint64_t o[NK][NT][2];                               // pairs of columns: rows g, g + 8
+  float ref_w[NT][2], ref_s[NT][2];
+  uint64_t l[NT];
 
   using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
 
@@ -274,12 +288,10 @@ struct Warp {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ref_w[nt][e] = ref_s[nt][e] = kNoRef;
-        l[nt][e] = 0.f;
-      }
+      for (int e = 0; e < 2; ++e) ref_w[nt][e] = ref_s[nt][e] = kNoRef;
+      l[nt] = 0;  // a pair of zeros
 #pragma unroll
-      for (int mt = 0; mt < NK; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+      for (int mt = 0; mt < NK; ++mt) o[mt][nt][0] = o[mt][nt][1] = 0;
     }
   }
 
@@ -287,7 +299,7 @@ struct Warp {
   // raises the references if need be, adds to l, and leaves the weights times
   // v_scale (mant * 2^ex) as operands pb[u][nt][high, low][2].  group != null:
   // the sum of p per unit and head goes to group[head * stride + at[u]] (at >= 0).
-  template <int U>
+  template <int U, bool WEIGHT>
   __device__ __forceinline__ void softmax(const float (&x)[U][NT][4], const float (&mant)[U],
                                           const float (&ex)[U], uint32_t (&pb)[U][NT][2][2],
                                           float2* group, int stride, const int (&at)[U],
@@ -312,7 +324,8 @@ struct Warp {
       }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float corr[2], fall[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float a = top_s[nt][e], b = top_w[nt][e];
@@ -323,33 +336,33 @@ struct Warp {
           }
           const float na = a > ref_s[nt][e] ? ceilf(a) + kHeadroom : ref_s[nt][e];
           const float nb = b > ref_w[nt][e] ? ceilf(b) + kHeadroom : ref_w[nt][e];
-          l[nt][e] *= ex2(ref_s[nt][e] - na);
-          const float corr = ex2(ref_w[nt][e] - nb);  // integers: exact
-#pragma unroll
-          for (int mt = 0; mt < NK; ++mt) {
-            o[mt][nt][e] *= corr;
-            o[mt][nt][e + 2] *= corr;
-          }
+          fall[e] = ex2(ref_s[nt][e] - na);
+          corr[e] = ex2(ref_w[nt][e] - nb);  // integers: exact
           ref_s[nt][e] = na;
           ref_w[nt][e] = nb;
         }
+        l[nt] = f32x2::mul(l[nt], f32x2::pack(fall[0], fall[1]));
+#pragma unroll
+        for (int mt = 0; mt < NK; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) o[mt][nt][i] = f32x2::mul(o[mt][nt][i], f32x2::pack(corr[0], corr[1]));
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4], sum[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p0 = ex2(x[u][nt][e] - ref_s[nt][e]), p1 = ex2(x[u][nt][e + 2] - ref_s[nt][e]);
-          sum[e] = p0 + p1;
-          l[nt][e] += sum[e];
-          const float r = ref_w[nt][e] - kWeightExp - ex[u];
-          w[e] = mant[u] * ex2(x[u][nt][e] - r);
-          w[e + 2] = mant[u] * ex2(x[u][nt][e + 2] - r);
-        }
-        const uint32_t h0 = pack_half2(w[0], w[1]), h1 = pack_half2(w[2], w[3]);
-        const uint32_t r0 = pack_rest(w[0], w[1], h0), r1 = pack_rest(w[2], w[3], h1);
+        const uint64_t x0 = f32x2::pack(x[u][nt][0], x[u][nt][1]), x1 = f32x2::pack(x[u][nt][2], x[u][nt][3]);
+        const uint64_t minus_s = f32x2::pack(-ref_s[nt][0], -ref_s[nt][1]);
+        const float up = kWeightExp + ex[u];
+        const uint64_t minus_w = f32x2::pack(up - ref_w[nt][0], up - ref_w[nt][1]);
+        const uint64_t m2 = f32x2::pack(mant[u], mant[u]);
+        const uint64_t sum = f32x2::add(ex2_pair(f32x2::add(x0, minus_s)), ex2_pair(f32x2::add(x1, minus_s)));
+        l[nt] = f32x2::add(l[nt], sum);
+        const float2 w0 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(x0, minus_w))));
+        const float2 w1 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(x1, minus_w))));
+        const uint32_t h0 = pack_half2(w0.x, w0.y), h1 = pack_half2(w1.x, w1.y);
+        const uint32_t r0 = pack_rest(w0.x, w0.y, h0), r1 = pack_rest(w1.x, w1.y, h1);
         if constexpr (GM == 4) {  // columns 0..3: high halves, 4..7: low halves
           pb[u][nt][0][0] = transpose8(c < 2 ? h0 : r0);
           pb[u][nt][0][1] = transpose8(c < 2 ? h1 : r1);
@@ -359,10 +372,11 @@ struct Warp {
           pb[u][nt][1][0] = transpose8(r0);
           pb[u][nt][1][1] = transpose8(r1);
         }
-        if (group) {
+        if constexpr (WEIGHT) {
+          const float2 both = f32x2::unpack(sum);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float s = sum[e];
+            float s = e ? both.y : both.x;
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
             const int head = nt * 8 + 2 * c + e;
@@ -453,7 +467,8 @@ struct Warp {
     const int at[1] = {unit};
     const bool kept[1] = {true};
     uint32_t pb[1][NT][2][2];
-    softmax<1>(x, mant, ex, pb, group, stride, at, kept, G);
+    if (group) softmax<1, true>(x, mant, ex, pb, group, stride, at, kept, G);
+    else softmax<1, false>(x, mant, ex, pb, group, stride, at, kept, G);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       float v[4][4];
@@ -476,15 +491,19 @@ struct Warp {
           }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(s, a[0], a[1], a[2], a[3], pb[0][nt][0][0], pb[0][nt][0][1]);
+          float s[4];
+          mma_zero(s, a[0], a[1], a[2], a[3], pb[0][nt][0][0], pb[0][nt][0][1]);
           if constexpr (GM != 4) mma(s, a[0], a[1], a[2], a[3], pb[0][nt][1][0], pb[0][nt][1][1]);
           if constexpr (kSplitQ) mma(s, b[0], b[1], b[2], b[3], pb[0][nt][0][0], pb[0][nt][0][1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[2 * j + half][nt][i] += s[i];
+          add_to(2 * j + half, nt, s);
         }
       }
     }
+  }
+
+  __device__ __forceinline__ void add_to(int mt, int nt, const float (&s)[4]) {
+    o[mt][nt][0] = f32x2::add(o[mt][nt][0], f32x2::pack(s[0], s[1]));
+    o[mt][nt][1] = f32x2::add(o[mt][nt][1], f32x2::pack(s[2], s[3]));
   }
 
   static __device__ __forceinline__ void unpack(const float4& v, float (&y)[4]) {
@@ -747,15 +766,14 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) load_shared(kt + Tile<D>::piece(Tile<D>::token(g + 8 * r), i * 4 + c), k[r][i]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[j][nt][0] = x[j][nt][1] = x[j][nt][2] = x[j][nt][3] = 0.f;
-#pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
           uint32_t a0, a1, a2, a3;
           widen4<FORMAT>(k[0][ks >> 2][ks & 3], a0, a2);
           widen4<FORMAT>(k[1][ks >> 2][ks & 3], a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma(x[j][nt], a0, a1, a2, a3, w.qh[nt][ks][0], w.qh[nt][ks][1]);
+            if (ks == 0) mma_zero(x[j][nt], a0, a1, a2, a3, w.qh[nt][ks][0], w.qh[nt][ks][1]);
+            else mma(x[j][nt], a0, a1, a2, a3, w.qh[nt][ks][0], w.qh[nt][ks][1]);
             if constexpr (W::kSplitQ) mma(x[j][nt], a0, a1, a2, a3, w.ql[nt][ks][0], w.ql[nt][ks][1]);
           }
         }
@@ -772,7 +790,8 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         kept[j] = unit.w >= 0.f;
       }
       uint32_t pb[kTile][NT][2][2];
-      w.template softmax<kTile>(x, mant, ex, pb, group, stride, at, kept, p.G);
+      if (group) w.template softmax<kTile, true>(x, mant, ex, pb, group, stride, at, kept, p.G);
+      else w.template softmax<kTile, false>(x, mant, ex, pb, group, stride, at, kept, p.G);
       uint32_t v[kTile][4][D / 32];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; D / 8 bytes at g D / 8
 #pragma unroll
       for (int j = 0; j < kTile; ++j)
@@ -797,15 +816,15 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[4];
 #pragma unroll
             for (int j = 0; j < kTile; ++j) {
               const uint32_t(&y)[4] = a[j][half];
-              mma(s, y[0], y[1], y[2], y[3], pb[j][nt][0][0], pb[j][nt][0][1]);
+              if (j == 0) mma_zero(s, y[0], y[1], y[2], y[3], pb[j][nt][0][0], pb[j][nt][0][1]);
+              else mma(s, y[0], y[1], y[2], y[3], pb[j][nt][0][0], pb[j][nt][0][1]);
               if constexpr (GM != 4) mma(s, y[0], y[1], y[2], y[3], pb[j][nt][1][0], pb[j][nt][1][1]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w.o[2 * i + half][nt][e] += s[e];
+            w.add_to(2 * i + half, nt, s);
           }
       }
       stage_scales();
@@ -824,13 +843,15 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float l = e ? f32x2::unpack(w.l[nt]).y : f32x2::unpack(w.l[nt]).x;
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) w.l[nt][e] += __shfl_xor_sync(0xffffffffu, w.l[nt][e], k);
+        for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
         const int head = nt * 8 + 2 * c + e;
         const bool mine = head < p.G && (GM != 4 || c < 2);
 #pragma unroll
         for (int mt = 0; mt < NK; ++mt) {
-          float y0 = w.o[mt][nt][e], y1 = w.o[mt][nt][e + 2];
+          const float2 p0 = f32x2::unpack(w.o[mt][nt][0]), p1 = f32x2::unpack(w.o[mt][nt][1]);
+          float y0 = e ? p0.y : p0.x, y1 = e ? p1.y : p1.x;
           if constexpr (GM == 4) {  // the low halves' columns
             y0 += __shfl_xor_sync(0xffffffffu, y0, 2);
             y1 += __shfl_xor_sync(0xffffffffu, y1, 2);
@@ -839,7 +860,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
         if (mine && g == 0)
           *reinterpret_cast<float4*>(ws.stat + (part * 16 + head) * 4) =
-              make_float4(w.ref_w[nt][e], w.ref_s[nt][e], w.l[nt][e], 0.f);
+              make_float4(w.ref_w[nt][e], w.ref_s[nt][e], l, 0.f);
       }
   }
 }

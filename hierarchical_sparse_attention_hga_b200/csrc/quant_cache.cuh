@@ -74,12 +74,34 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t x) {
   return r;
 }
 
-// One code as a float.
-template <int FORMAT>
-__device__ __forceinline__ float code_to_f32(uint8_t c) {
-  if (FORMAT == kQuantInt8) return static_cast<float>(static_cast<int8_t>(c));
-  const uint32_t h = e4m3x2_to_half2(c);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffff)));
+// Two floats in one register pair; each half of an operation is rounded as the
+// scalar one, at half the instructions.
+namespace f32x2 {
+__device__ __forceinline__ uint64_t pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ float2 unpack(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+}  // namespace f32x2
 
 }  // namespace hga
