@@ -158,15 +158,31 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
 // 2^n for an integer n in [-126, 127].
 __device__ __forceinline__ float exp2i(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 
-// Exponent e (clamped to [-100, 127]) of the largest finite |value|'s bits, so
-// that value * 2^(14 - e) is below 2^15; 0 for all-zero input.
+// Exponent e (clamped to [-100, 127]) of the largest |value|'s bits, so that
+// value * 2^(14 - e) is below 2^15; 0 for all-zero input.
 __device__ __forceinline__ int scale_exponent(uint32_t top_bits) {
   return top_bits == 0 ? 0 : max(static_cast<int>(top_bits >> 23) - 127, -100);
 }
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The largest |element| of rows as bits (NaN above infinity above the finite ones),
+// four at a time.
+struct TopBf16 {
+  uint32_t top = 0;
+  __device__ __forceinline__ void add(const uint2& r) {
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(r.x & 0x7fff7fffu));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(r.y & 0x7fff7fffu));
+  }
+  __device__ __forceinline__ uint32_t bits() const { return max(top << 16, top & 0xffff0000u); }
+};
+struct TopF32 {
+  uint32_t top = 0;
+  __device__ __forceinline__ void add(const float4& r) {
+    top = max(max(top, __float_as_uint(r.x) & 0x7fffffffu), __float_as_uint(r.y) & 0x7fffffffu);
+    top = max(max(top, __float_as_uint(r.z) & 0x7fffffffu), __float_as_uint(r.w) & 0x7fffffffu);
+  }
+  __device__ __forceinline__ uint32_t bits() const { return top; }
+};
 
 // v_scale as mant * 2^ex.
 __device__ __forceinline__ void split_scale(float v, float& mant, float& ex) {
@@ -237,6 +253,7 @@ struct Warp {
   uint64_t l[NT];
 
   using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
+  using Top = typename std::conditional<kSplitQ, TopF32, TopBf16>::type;
 
   // Query heads of (b, h): column n of tile nt is head nt * 8 + n; with GM == 4
   // columns 4..7 repeat heads 0..3.
@@ -255,30 +272,29 @@ struct Warp {
     const int lane = threadIdx.x & 31, c = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float x[NK][4];
-      uint32_t top = 0;
+      Top most;
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        unpack(raw[nt][ks], x[ks]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, finite_bits(x[ks][i]));
-      }
+      for (int ks = 0; ks < NK; ++ks) most.add(raw[nt][ks]);
+      uint32_t top = most.bits();
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = scale_exponent(top);
+      const int e = top < kInfBits ? scale_exponent(top) : 0;
       const float up = exp2i(14 - e);
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
+        float x[4];
+        unpack(raw[nt][ks], x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[ks][i] *= up;
-        qh[nt][ks][0] = pack_half2(x[ks][0], x[ks][1]);
-        qh[nt][ks][1] = pack_half2(x[ks][2], x[ks][3]);
+        for (int i = 0; i < 4; ++i) x[i] *= up;
+        qh[nt][ks][0] = pack_half2(x[0], x[1]);
+        qh[nt][ks][1] = pack_half2(x[2], x[3]);
         if constexpr (kSplitQ) {
-          ql[nt][ks][0] = pack_rest(x[ks][0], x[ks][1], qh[nt][ks][0]);
-          ql[nt][ks][1] = pack_rest(x[ks][2], x[ks][3], qh[nt][ks][1]);
+          ql[nt][ks][0] = pack_rest(x[0], x[1], qh[nt][ks][0]);
+          ql[nt][ks][1] = pack_rest(x[2], x[3], qh[nt][ks][1]);
         }
       }
-      const float down = exp2i(e - 14) * (kLog2e * rsqrtf(static_cast<float>(D)));
+      // a query with an infinity or NaN makes its head NaN
+      const float down = top < kInfBits ? exp2i(e - 14) * (kLog2e * rsqrtf(static_cast<float>(D))) : CUDART_NAN_F;
       f[nt][0] = __shfl_sync(0xffffffffu, down, 8 * c);       // column 2c is lane group g = 2c
       f[nt][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
     }
@@ -410,26 +426,21 @@ struct Warp {
         if (row < rest) vr[r][j] = *reinterpret_cast<const Row*>(vt + row * D + g * (D / 8) + 4 * j);
       }
     }
-    uint32_t top_k = 0, top_v = 0;
-    float y[4];
+    Top most_k, most_v;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        unpack(kr[r][ks], y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top_k = max(top_k, finite_bits(y[i]));
-      }
+      for (int ks = 0; ks < NK; ++ks) most_k.add(kr[r][ks]);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        unpack(vr[r][j], y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top_v = max(top_v, finite_bits(y[i]));
-      }
-    const int e_k = scale_exponent(__reduce_max_sync(0xffffffffu, top_k));
-    const int e_v = scale_exponent(__reduce_max_sync(0xffffffffu, top_v));
+      for (int j = 0; j < D / 32; ++j) most_v.add(vr[r][j]);
+    const uint32_t top_k = __reduce_max_sync(0xffffffffu, most_k.bits());
+    const uint32_t top_v = __reduce_max_sync(0xffffffffu, most_v.bits());
+    // as the group will once it is closed, a tail with an infinity or NaN makes NaN
+    const bool finite = max(top_k, top_v) < kInfBits;
+    const int e_k = finite ? scale_exponent(top_k) : 0, e_v = finite ? scale_exponent(top_v) : 0;
+    float y[4];
     const float up_k = exp2i(14 - e_k), down_k = exp2i(e_k - 14), up_v = exp2i(14 - e_v);
     float x[1][NT][4];
 #pragma unroll
@@ -462,7 +473,7 @@ struct Warp {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[0][nt][i] = g + 8 * (i >> 1) < rest ? x[0][nt][i] * (f[nt][i & 1] * down_k) : -CUDART_INF_F;
+        x[0][nt][i] = !finite ? CUDART_NAN_F : g + 8 * (i >> 1) < rest ? x[0][nt][i] * (f[nt][i & 1] * down_k) : -CUDART_INF_F;
     const float mant[1] = {1.f}, ex[1] = {static_cast<float>(e_v - 14)};
     const int at[1] = {unit};
     const bool kept[1] = {true};
@@ -531,7 +542,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   // per unit, two blocks of 32: k_scale, v_scale as mantissa and exponent, state (1: in
   // the ring, 0: no tokens, -1: id not kept)
   __shared__ float4 s_units[kWarps][2][32];
-  __shared__ int64_t s_before[kThreads];                // list length before each thread's items
+  __shared__ int64_t s_before[kThreads];                // list length before each thread's rows
   __shared__ int64_t s_all;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   uint8_t* ring = s_rings + warp * kRing;
@@ -556,18 +567,21 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int64_t slices = static_cast<int64_t>(gridDim.x) * kWarps;
     return max(static_cast<int64_t>(kMinSlice), (all + slices - 1) / slices);
   };
-  // an item's length in the list of all items' units, its fixed work in front
-  auto item_length = [&](int i, unsigned* e) {
-    const int64_t pb = pos[i / p.Hkv];
-    const int n = units_of(p, quant_item(qc, pb, i, e), pb, group_idx != nullptr).total;
+  // The list's rows are the sequences, whose `same` KV heads have equal lengths, or,
+  // where eviction may have made them differ, the items.  An item's length in the
+  // list: its units, its fixed work in front.
+  const int same = qc.evicted ? 1 : p.Hkv, rows = qc.evicted ? items : p.B;
+  auto item_length = [&](int row, unsigned* e) {
+    const int64_t pb = pos[qc.evicted ? row / p.Hkv : row];
+    const int n = units_of(p, quant_item(qc, pb, row, e), pb, group_idx != nullptr).total;
     return n ? n + kItemCost : 0;
   };
   // where this warp's slice [lo, hi) of the list begins
-  const int per = (items + kThreads - 1) / kThreads;
+  const int per = (rows + kThreads - 1) / kThreads;
   {
     int64_t mine = 0;
-    for (int i = min(items, tid * per); i < min(items, (tid + 1) * per); ++i)
-      mine += item_length(i, blockIdx.x == 0 ? err : nullptr);
+    for (int i = min(rows, tid * per); i < min(rows, (tid + 1) * per); ++i)
+      mine += static_cast<int64_t>(item_length(i, blockIdx.x == 0 ? err : nullptr)) * same;
     s_before[tid] = mine;
     __syncthreads();
     if (warp == 0) {
@@ -604,13 +618,13 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       return;
     }
     left = static_cast<int>(min(slice, all - lo));
-    int owner = -1;  // the last thread whose items begin at or before lo
+    int owner = -1;  // the last thread whose rows begin at or before lo
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) owner += __popc(__ballot_sync(0xffffffffu, s_before[j * 32 + lane] <= lo));
-    int64_t start = s_before[owner];  // where the item begins in the list
-    for (item = owner * per;; item += 32) {
-      const int n = item + lane < items ? item_length(item + lane, nullptr) : 0;
-      int64_t x = n;
+    int64_t start = s_before[owner];  // where the row begins in the list
+    for (int row = owner * per;; row += 32) {
+      const int n = row + lane < rows ? item_length(row + lane, nullptr) : 0;
+      int64_t x = static_cast<int64_t>(n) * same;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -618,14 +632,15 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       const unsigned beyond = __ballot_sync(0xffffffffu, start + x > lo);
       if (beyond) {
-        const int j = __ffs(beyond) - 1;
-        start += __shfl_sync(0xffffffffu, x - n, j);
-        item += j;
+        const int j = __ffs(beyond) - 1, length = __shfl_sync(0xffffffffu, n, j);
+        start += __shfl_sync(0xffffffffu, x - static_cast<int64_t>(n) * same, j);
+        const int head = static_cast<int>(static_cast<uint64_t>(lo - start) / static_cast<uint32_t>(length));
+        item = (row + j) * same + head;
+        skip = static_cast<int>(lo - start - static_cast<int64_t>(head) * length);
         break;
       }
       start += __shfl_sync(0xffffffffu, x, 31);
     }
-    skip = static_cast<int>(lo - start);
   }
 
   W w;

@@ -619,6 +619,8 @@ hga_status hga_quant_append(const hga_config* cfg, const hga_quant_cache* cache,
  *   workspace  device scratch of hga_quant_attend_workspace_size(cfg,
  *              max_groups, weight_out != NULL) bytes, 16-byte aligned; calls
  *              that may overlap need their own
+ * A query that holds an infinity or NaN makes its head's outputs NaN; so do, for
+ * every head, an attended group that held one and a tail that holds one.
  * A sequence with no tokens gets zeros and an LSE of -inf.  A bad position, table
  * entry or group id is flagged and skipped as in hga_attend.  Sums are float32;
  * the softmax weights enter the products with 22 bits, the codes exactly.  The

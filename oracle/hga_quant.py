@@ -77,6 +77,9 @@ class Item:
         k, v = self.rows("k", entries), self.rows("v", entries)
         if not len(k):
             return np.zeros(q.shape), np.full(len(q), -np.inf), weight
+        # a tail that holds an infinity or NaN stands as the group that it will be
+        if not (np.isfinite(self.k_tail).all() and np.isfinite(self.v_tail).all()):
+            return np.full(q.shape, np.nan), np.full(len(q), np.nan), np.full(n_units, np.nan)
         with np.errstate(invalid="ignore"):        # a group that holds a NaN makes NaN
             s = q @ k.T / math.sqrt(self.dim)
             top = s.max(1, keepdims=True)

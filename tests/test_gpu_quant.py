@@ -361,6 +361,37 @@ def test_attend_tail_values():
         c.check_attend(q, c.attend(q))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_attend_what_is_not_finite(dtype, bad):
+    """An infinity or NaN in the tail's K or V makes the item's heads NaN, as the closed group
+    does; one in a query its own head; other items and heads keep their bits."""
+    for where in ("k", "v", "q"):
+        c = Cache(2, 2, 64, 4, dtype, heads_q=6, seed=23)
+        k, v = c.rng.standard_normal((2, 2, 2, 41, 64))
+        q = c.q()
+        clean = Cache(2, 2, 64, 4, dtype, heads_q=6, seed=23)
+        clean.append(k, v)
+        right = clean.attend(q)
+        if where == "q":
+            q[1, 4, 0, 3] = bad
+            hit = [(1, 4)]
+        else:
+            (k if where == "k" else v)[0, 1, 35, 5] = bad
+            hit = [(0, 3), (0, 4), (0, 5)]
+        c.append(k, v)
+        got = c.attend(q)
+        for b in range(2):
+            for head in range(6):
+                if (b, head) in hit:
+                    assert torch.isnan(got[0][b, head]).all() and torch.isnan(got[1][b, head]).all()
+                else:
+                    assert torch.equal(got[0][b, head], right[0][b, head]) and torch.equal(got[1][b, head], right[1][b, head])
+        if where != "q":
+            out, lse, weight = c.items[0][1].attend(stored(q[0, 3:6, 0], dtype))
+            assert np.isnan(out).all() and np.isnan(lse).all()
+
+
 def routed_ids(rng, n, kg, chunk, sink, local):
     per, cur = chunk // 16, max(0, n - 1) // chunk
     lo, hi = sink * per, max(0, cur - local) * per
