@@ -265,7 +265,7 @@ struct Warp {
       const T* row = q + (static_cast<int64_t>(b) * p.Hq + h * p.G + head) * D + c * 16;
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks)
-        raw[nt][ks] = head < p.G ? __ldg(reinterpret_cast<const Row*>(row + (ks >> 2) * 64 + (ks & 3) * 4)) : Row{};
+        raw[nt][ks] = head < p.G ? *reinterpret_cast<const Row*>(row + (ks >> 2) * 64 + (ks & 3) * 4) : Row{};
     }
   }
   __device__ __forceinline__ void load_q(const Row (&raw)[NT][NK]) {
@@ -529,9 +529,8 @@ struct Warp {
 template <typename T, int D, int FORMAT, int GM>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(GM))
 quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    LayerParams p, QuantCache qc, const T* __restrict__ q,
-                    const int64_t* __restrict__ pos, const int32_t* __restrict__ group_idx,
-                    Workspace ws, unsigned* err) {
+                    LayerParams p, QuantCache qc, const T* q, const int64_t* __restrict__ pos,
+                    const int32_t* group_idx, Workspace ws, unsigned* err) {
   using W = Warp<T, D, FORMAT, GM>;
   constexpr int NT = W::NT, NK = W::NK;
   constexpr int kUnitBytes = Tile<D>::kUnitBytes;
@@ -558,7 +557,8 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   }
   // What kernels of this library write is read, and the scratch that the merge of
   // an earlier call may still read is written, behind pdl_wait: the counts of
-  // evicted groups first of all.  Positions and queries come before it.
+  // evicted groups first of all.  Only positions come before it (a query may be
+  // another call's output).
   bool waited = qc.evicted != nullptr;
   if (waited) pdl_wait();
 
@@ -658,12 +658,12 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (u_hi <= 0) break;  // only the item's fixed part
     left -= un.total + kItemCost - skip;
     skip = 0;
-    typename W::Row q_raw[NT][NK];
-    w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
     if (!waited) {
       pdl_wait();
       waited = true;
     }
+    typename W::Row q_raw[NT][NK];
+    w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
     pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
     if (lane == 0 && u_lo == 0) {  // this warp has the item's first unit; its last one is total - u_hi further on
       const int64_t slice = slice_length(s_all);
@@ -888,7 +888,7 @@ constexpr int merge_warps(int split) { return split > 1 ? split : 8; }
 template <int D, typename TO, int SPLIT>
 __global__ void __launch_bounds__(merge_warps(SPLIT) * 32)
 quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos, Workspace ws,
-                   const int32_t* __restrict__ group_idx, const float* weight_in,
+                   const int32_t* group_idx, const float* weight_in,
                    float* weight_out, TO* __restrict__ out,
                    float* __restrict__ lse) {
   constexpr int kMergeWarps = merge_warps(SPLIT), kMergeThreads = kMergeWarps * 32;
