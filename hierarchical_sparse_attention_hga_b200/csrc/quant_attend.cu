@@ -979,11 +979,12 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
     }
     if (on && share == 0) {
       const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + head;
-      // acc is in units of 2^(rw - 14), l in units of 2^rs
-      const float scale = l == 0.f ? 0.f : ex2(rw - kWeightExp - rs) / l;
+      // acc is in units of 2^(rw - 14), l in units of 2^rs; two factors, since 2^(rw - rs)
+      // may be as small or large as the values
+      const float inverse = l == 0.f ? 0.f : ex2(-kWeightExp) / l, scale = ex2(rw - rs);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j)
-        store_out(out + row * D + dim_of<D>(j * 32 + lane), l == 0.f ? 0.f : acc[j] * scale);
+        store_out(out + row * D + dim_of<D>(j * 32 + lane), l == 0.f ? 0.f : acc[j] * inverse * scale);
       if (lse && lane == 0) lse[row] = l == 0.f ? -CUDART_INF_F : (rs + log2f(l)) * kLn2;
     }
   } else {

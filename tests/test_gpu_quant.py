@@ -348,15 +348,19 @@ def test_attend_uneven_scales(dtype, fmt):
 
 
 def test_attend_tail_values():
-    """Tails of tiny, large and zero rows, beside closed groups and alone."""
+    """Tails of tiny, large and zero rows, beside closed groups and alone; values as small and as
+    large as a tail's scale goes."""
     for dtype in ("bf16", "f32"):
-        c = Cache(4, 1, 64, 4, dtype, heads_q=3, seed=10)
-        k, v = c.rng.standard_normal((2, 4, 1, 27, 64))
+        c = Cache(7, 1, 64, 4, dtype, heads_q=3, seed=10)
+        k, v = c.rng.standard_normal((2, 7, 1, 27, 64))
         k[0] *= 1e-25
         v[1] *= 1e25
         v[2, 0, 16:] = 0
         k[3, 0, 20:] *= 50
-        c.append(k, v, [27, 27, 27, 9])
+        v[4] *= 1e-30
+        v[5] *= 2.0 ** -110
+        v[6] *= 1e36
+        c.append(k, v, [27, 27, 27, 9, 27, 11, 5])
         q = c.q()
         c.check_attend(q, c.attend(q))
 
