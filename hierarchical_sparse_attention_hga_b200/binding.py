@@ -154,6 +154,14 @@ def _ptr(x):
     return x.ctypes.data
 
 
+def _dense(x):
+    """_ptr of a tensor that has to be contiguous (a slice of a larger one often is not)."""
+    check = getattr(x, "is_contiguous", None)
+    if check is not None and not check():
+        raise ValueError("tensors passed to the library must be contiguous")
+    return _ptr(x)
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -433,15 +441,16 @@ def quant_cache(k, v, k_scale, v_scale, k_tail, v_tail, table, n_slots: int, max
                 format: int = HGA_QUANT_E4M3, evicted=None) -> HGAQuantCache:
     """An 8-bit K/V cache's description (struct hga_quant_cache): pools of n_slots groups, the
     table [B, Hkv, max_groups] and the tails.  The caller keeps the tensors alive."""
-    return HGAQuantCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_tail),
-                         _ptr(v_tail), _ptr(table), _ptr(evicted), n_slots, max_groups, format)
+    return HGAQuantCache(_dense(k), _dense(v), _dense(k_scale), _dense(v_scale), _dense(k_tail),
+                         _dense(v_tail), _dense(table), _dense(evicted), n_slots, max_groups,
+                         format)
 
 
 def hga_quant_append(cfg, cache: HGAQuantCache, k_new, v_new, n_new: int, pos, counts=None,
                      chunk_sum=None, group_sum=None, stream=None) -> None:
     """Writes new rows into an 8-bit cache (tail, closed groups, optional summary rows)."""
     _check(load_library().hga_quant_append(ctypes.byref(_cfg(cfg)), ctypes.byref(cache),
-                                           _ptr(k_new), _ptr(v_new), n_new, _ptr(counts),
+                                           _dense(k_new), _dense(v_new), n_new, _ptr(counts),
                                            _ptr(pos), _ptr(chunk_sum), _ptr(group_sum),
                                            _stream(stream)), "hga_quant_append")
 
@@ -459,9 +468,9 @@ def hga_quant_attend(cfg, cache: HGAQuantCache, q, pos, out, lse=None, group_idx
                      stream=None) -> None:
     """Decode attention over an 8-bit cache: every live group, or the routed sets of group_idx;
     weight_out = weight_in + each group's attention weight."""
-    _check(load_library().hga_quant_attend(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _ptr(q),
+    _check(load_library().hga_quant_attend(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _dense(q),
                                            _ptr(pos), _ptr(group_idx), _ptr(weight_in),
-                                           _ptr(weight_out), _ptr(out), _ptr(lse),
+                                           _ptr(weight_out), _dense(out), _ptr(lse),
                                            _ptr(workspace), workspace_bytes, _stream(stream)),
            "hga_quant_attend")
 

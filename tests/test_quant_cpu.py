@@ -192,3 +192,21 @@ def test_evict_arguments():
         refused(1, B.hga_quant_evict, layer, cache(), a[0], 4, 1, 1, *a[1:])
     refused(3, B.hga_quant_evict, layer, cache(max_groups=49153, n_slots=1 << 20), 16, 4, 1, 1, 16,
             16, 16, 16)
+
+
+def test_slices_of_larger_tensors_are_refused():
+    """The calls take whole arrays: a slice of a batch that is not contiguous would be read
+    wrongly."""
+    layer = B.Layer(**LAYER)
+    big = torch.zeros(2, 2, 64, 128, dtype=torch.bfloat16)
+    part = big[:, :, :16]
+    whole = part.contiguous()
+    with pytest.raises(ValueError):
+        cache(k_tail=part)
+    with pytest.raises(ValueError):
+        B.hga_quant_append(layer, cache(), part, whole, 16, 16, stream=0)
+    with pytest.raises(ValueError):
+        B.hga_quant_append(layer, cache(), whole, part, 16, 16, stream=0)
+    for q, out in ((part, whole), (whole, part)):
+        with pytest.raises(ValueError):
+            B.hga_quant_attend(layer, cache(), q, 16, out, stream=0)
