@@ -29,9 +29,12 @@
 // v_scale, are split into two halves as well (22 bits): with at most four heads
 // the low halves take the unused four columns, for free.  References of the
 // running softmax are integers, so every rescaling is exact, and v_scale enters
-// as exponent and mantissa, so its size never costs bits.  Each tile's product
-// starts from zero and is added to the running sum in float32 (round to
-// nearest): the matrix unit's own accumulation is never longer than a tile.
+// as exponent and mantissa, so its size never costs bits.  A weight's reference
+// (of p v_scale) is kept as its distance from the score's, and the exponents of
+// weights are sums of distances: beyond 2^24 a score has no bits left to which an
+// exponent could be added.  Each tile's product starts from zero and is added to the
+// running sum in float32 (round to nearest): the matrix unit's own accumulation is
+// never longer than a tile.
 //
 // Work.  A fixed grid; the units (groups, and one for a tail) of all items form
 // one list, of which each warp takes an equal slice, whatever the sequences'
@@ -63,7 +66,7 @@ constexpr int kMinSlice = 2;         // units a warp takes at least (a 1K prompt
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kWaitLimit = 1u << 26;  // bounded mbarrier polls (and 50 ms)
-constexpr float kNoRef = -1e30f;     // reference before the first score
+constexpr float kNoRef = -3e38f;     // reference before the first score
 constexpr float kHeadroom = 2.f;     // a raised reference exceeds the maximum by 2 to 3
 constexpr float kWeightExp = 14.f;   // weights are at most 2 * 2^(14 - 2) in f16
 
@@ -232,7 +235,7 @@ __device__ __forceinline__ Units units_of(const LayerParams& p, const QuantItem&
 // Scratch of one call.
 struct Workspace {
   int2* parts;     // [items]: first warp of the item, number of warps
-  float* stat;     // [warps + items][16][4]: weight reference, score reference, denominator
+  float* stat;     // [warps + items][16][4]: weight reference less the score's, score reference, denominator
   float* sum;      // [warps + items][G][D], dimensions in the kernel's order
   float2* group;   // [items][G][max_groups + kg]: each unit's sum (-1: a routed id that is not
                    // kept) and its reference, in the virtual list's order (weights only)
@@ -254,7 +257,7 @@ struct Warp {
   uint32_t qh[NT][NK][2], ql[kSplitQ ? NT : 1][kSplitQ ? NK : 1][2];
   float f[NT][2];                                      // score scale of this lane's columns (log2 units)
   uint64_t o[NK][NT][2];                               // pairs of columns: rows g, g + 8
-  float ref_w[NT][2], ref_s[NT][2];
+  float ref_s[NT][2], lift[NT][2];                     // references: scores, and scores times v_scale less ref_s
   uint64_t l[NT];
 
   using Row = typename std::conditional<kSplitQ, float4, uint2>::type;  // four values
@@ -309,7 +312,10 @@ struct Warp {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref_w[nt][e] = ref_s[nt][e] = kNoRef;
+      for (int e = 0; e < 2; ++e) {
+        ref_s[nt][e] = kNoRef;
+        lift[nt][e] = 0.f;
+      }
       l[nt] = 0;  // a pair of zeros
 #pragma unroll
       for (int mt = 0; mt < NK; ++mt) o[mt][nt][0] = o[mt][nt][1] = 0;
@@ -326,7 +332,6 @@ struct Warp {
                                           float2* group, int stride, const int (&at)[U],
                                           const bool (&kept)[U], int G) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float top_s[NT][2], top_w[NT][2];
     bool raise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -335,13 +340,11 @@ struct Warp {
         float a = -CUDART_INF_F, b = -CUDART_INF_F;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const float y = fmaxf(x[u][nt][e], x[u][nt][e + 2]);
+          const float y = fmaxf(x[u][nt][e], x[u][nt][e + 2]) - ref_s[nt][e];
           a = fmaxf(a, y);
           b = fmaxf(b, y + ex[u]);
         }
-        top_s[nt][e] = a;
-        top_w[nt][e] = b;
-        raise |= a > ref_s[nt][e] || b > ref_w[nt][e];
+        raise |= a > 0.f || b > lift[nt][e];
       }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -349,18 +352,23 @@ struct Warp {
         float corr[2], fall[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float a = top_s[nt][e], b = top_w[nt][e];
+          float a = -CUDART_INF_F, b = -CUDART_INF_F;
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) {
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
-          }
+          for (int u = 0; u < U; ++u) a = fmaxf(a, fmaxf(x[u][nt][e], x[u][nt][e + 2]));
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
           const float na = a > ref_s[nt][e] ? ceilf(a) + kHeadroom : ref_s[nt][e];
-          const float nb = b > ref_w[nt][e] ? ceilf(b) + kHeadroom : ref_w[nt][e];
-          fall[e] = ex2(ref_s[nt][e] - na);
-          corr[e] = ex2(ref_w[nt][e] - nb);  // integers: exact
+#pragma unroll
+          for (int u = 0; u < U; ++u) b = fmaxf(b, fmaxf(x[u][nt][e], x[u][nt][e + 2]) - na + ex[u]);
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
+          const float by = na - ref_s[nt][e];
+          const float held = lift[nt][e] - by;  // the weight's reference where it was
+          const float nb = b > held ? ceilf(b) + kHeadroom : held;
+          fall[e] = ex2(-by);
+          corr[e] = ex2(held - nb);  // integers: exact
           ref_s[nt][e] = na;
-          ref_w[nt][e] = nb;
+          lift[nt][e] = nb;
         }
         l[nt] = f32x2::mul(l[nt], f32x2::pack(fall[0], fall[1]));
 #pragma unroll
@@ -373,15 +381,16 @@ struct Warp {
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint64_t x0 = f32x2::pack(x[u][nt][0], x[u][nt][1]), x1 = f32x2::pack(x[u][nt][2], x[u][nt][3]);
-        const uint64_t minus_s = f32x2::pack(-ref_s[nt][0], -ref_s[nt][1]);
+        const uint64_t minus = f32x2::pack(-ref_s[nt][0], -ref_s[nt][1]);
+        const uint64_t y0 = f32x2::add(f32x2::pack(x[u][nt][0], x[u][nt][1]), minus);
+        const uint64_t y1 = f32x2::add(f32x2::pack(x[u][nt][2], x[u][nt][3]), minus);
         const float up = kWeightExp + ex[u];
-        const uint64_t minus_w = f32x2::pack(up - ref_w[nt][0], up - ref_w[nt][1]);
+        const uint64_t more = f32x2::pack(up - lift[nt][0], up - lift[nt][1]);
         const uint64_t m2 = f32x2::pack(mant[u], mant[u]);
-        const uint64_t sum = f32x2::add(ex2_pair(f32x2::add(x0, minus_s)), ex2_pair(f32x2::add(x1, minus_s)));
+        const uint64_t sum = f32x2::add(ex2_pair(y0), ex2_pair(y1));
         l[nt] = f32x2::add(l[nt], sum);
-        const float2 w0 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(x0, minus_w))));
-        const float2 w1 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(x1, minus_w))));
+        const float2 w0 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(y0, more))));
+        const float2 w1 = f32x2::unpack(f32x2::mul(m2, ex2_pair(f32x2::add(y1, more))));
         const uint32_t h0 = pack_half2(w0.x, w0.y), h1 = pack_half2(w1.x, w1.y);
         const uint32_t r0 = pack_rest(w0.x, w0.y, h0), r1 = pack_rest(w1.x, w1.y, h1);
         if constexpr (GM == 4) {  // columns 0..3: high halves, 4..7: low halves
@@ -880,7 +889,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         }
         if (mine && g == 0)
           *reinterpret_cast<float4*>(ws.stat + (part * 16 + head) * 4) =
-              make_float4(w.ref_w[nt][e], w.ref_s[nt][e], l, 0.f);
+              make_float4(w.lift[nt][e], w.ref_s[nt][e], l, 0.f);
       }
   }
 }
@@ -918,7 +927,7 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
   if (static_cast<int>(blockIdx.y) < head_blocks) {
     const int head = blockIdx.y * kHeads + warp / SPLIT, share = warp % SPLIT;
     const bool on = head < p.G;
-    float rw = kNoRef, rs = kNoRef, acc[D / 32], l = 0.f;
+    float rw = 0.f, rs = kNoRef, acc[D / 32], l = 0.f;  // as in a partial: rw counts from rs
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
     const float* rows = ws.sum + (first * p.G + head) * D + lane;
@@ -930,18 +939,22 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k * SPLIT;
-        s[k] = make_float4(kNoRef, kNoRef, 0.f, 0.f);
+        s[k] = make_float4(0.f, kNoRef, 0.f, 0.f);
         if (i < count) s[k] = stat[i * 16 + head];
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) x[k][j] = i < count ? rows[static_cast<int64_t>(i) * p.G * D + j * 32] : 0.f;
       }
-      float nw = rw, ns = rs;
+      float ns = rs;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) ns = fmaxf(ns, s[k].y);
+      const float held = rw + (rs - ns);
+      float nw = held;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
+        s[k].x += s[k].y - ns;
         nw = fmaxf(nw, s[k].x);
-        ns = fmaxf(ns, s[k].y);
       }
-      const float fw = ex2(rw - nw);
+      const float fw = ex2(held - nw);
       l *= ex2(rs - ns);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) acc[j] *= fw;
@@ -962,11 +975,12 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
       __syncthreads();
       if (share == 0) {
         static_assert(SPLIT <= 32, "a lane for every warp");
-        const float4 s = lane < SPLIT ? s_warp[lane] : make_float4(kNoRef, kNoRef, 0.f, 0.f);
-        rw = warp_max(s.x);
+        const float4 s = lane < SPLIT ? s_warp[lane] : make_float4(0.f, kNoRef, 0.f, 0.f);
         rs = warp_max(s.y);
+        const float above = s.x + (s.y - rs);
+        rw = warp_max(above);
         l = warp_sum(s.z * ex2(s.y - rs));
-        const float f = ex2(s.x - rw);
+        const float f = ex2(above - rw);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
 #pragma unroll 8
@@ -979,9 +993,9 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
     }
     if (on && share == 0) {
       const int64_t row = static_cast<int64_t>(b) * p.Hq + h * p.G + head;
-      // acc is in units of 2^(rw - 14), l in units of 2^rs; two factors, since 2^(rw - rs)
+      // acc is in units of 2^(rs + rw - 14), l in units of 2^rs; two factors, since 2^rw
       // may be as small or large as the values
-      const float inverse = l == 0.f ? 0.f : ex2(-kWeightExp) / l, scale = ex2(rw - rs);
+      const float inverse = l == 0.f ? 0.f : ex2(-kWeightExp) / l, scale = ex2(rw);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j)
         store_out(out + row * D + dim_of<D>(j * 32 + lane), l == 0.f ? 0.f : acc[j] * inverse * scale);

@@ -726,3 +726,50 @@ def test_two_graphs_on_two_streams():
         for t, x in zip(state, want):
             assert torch.equal(torch.nan_to_num(t.float()), torch.nan_to_num(x.float()))
     assert B.hga_device_status() == 0
+
+
+# ---- scores that leave float32 no fraction
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype,fmt,product", [
+    ("bf16", "e4m3", 1e5), ("bf16", "int8", 1e6), ("f32", "e4m3", 1e8), ("bf16", "e4m3", 1e12),
+    ("f32", "int8", 1e20), ("bf16", "e4m3", 1e30), ("f32", "e4m3", 1e34)])
+def test_attend_scores_far_beyond_one_another(dtype, fmt, product, sign):
+    """One token's score above the others' by millions to 1e35, all of them positive or all
+    negative: its value is the output, whatever the size of its group's values.
+
+    The softmax weight is 1 and the others' are 0 in 64 bits too, so only the arithmetic behind the
+    score counts: two exponentials of 2 ulp (each 2^-23), 22 bits in the product, the division and
+    the scales: 2^-20 in all, as in `bounds`.  A tail's values are held to 2^-39 of its largest.  The LSE is
+    the score, a sum of D + 8 products summed within 2^-22 of their size."""
+    size = product ** 0.5
+    for at, lens in ((100, [333, 2000]), (331, [333, 2000]), (1999, [2000, 2000])):
+        c = Cache(2, 2, 128, 130, dtype, fmt, heads_q=6, seed=31)
+        n = max(lens)
+        u = c.rng.choice([-1.0, 1.0], 128)
+        k, v = c.rng.standard_normal((2, 2, 2, n, 128))
+        if sign < 0:
+            k = (2 + np.abs(k[..., :1])) * u
+        for g in range(n // 16 + 1):
+            v[:, :, 16 * g:16 * g + 16] *= 2.0 ** c.rng.integers(-20, 21)
+        k[:, :, at] = (2.0 if sign > 0 else 0.5) * u
+        c.append(size * k, v, lens)
+        q = np.broadcast_to(sign * size * u, (2, 6, 1, 128)) * np.linspace(1, 2, 6)[None, :, None, None]
+        w_in = torch.zeros(2, 2, 130, device="cuda")
+        w_out = torch.full_like(w_in, -5)
+        out, lse = (t.double().cpu().numpy() for t in c.attend(q, weight=w_in, weight_out=w_out))
+        assert B.hga_device_status() == 0
+        w_out = w_out.cpu().numpy()
+        for b in range(2):
+            if at >= lens[b]:
+                continue
+            for h in range(2):
+                it = c.items[b][h]
+                rows = slice(3 * h, 3 * h + 3)
+                want, want_lse, weight = it.attend(stored(q[b, rows, 0], dtype))
+                assert np.count_nonzero(weight) == 1 and weight.max() == 3
+                tol = 2.0 ** -20 * np.abs(want) + 2.0 ** -38 * np.abs(it.rows("v", range(len(it.v)))[at // 16 * 16:][:16]).max()
+                assert (np.abs(out[b, rows, 0] - want) <= tol).all(), (b, h, at)
+                assert (np.abs(lse[b, rows, 0] - want_lse) <= (136 + 2) * 2.0 ** -22 * np.abs(want_lse)).all()
+                np.testing.assert_allclose(w_out[b, h, :len(weight)], weight, rtol=2.0 ** -20, atol=0)
