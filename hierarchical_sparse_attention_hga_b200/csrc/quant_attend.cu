@@ -218,25 +218,27 @@ struct Units {
   }
 };
 
-__device__ __forceinline__ Units units_of(const LayerParams& p, const QuantItem& it, int64_t pos,
-                                          bool routed) {
-  Units u{0, 0, it.closed, it.closed, it.units()};
-  if (routed && u.total) {
-    const int first = max(0, static_cast<int>(pos / p.C) - p.local);
+// tokens: live ones of the item, those of the groups and of the tail
+__device__ __forceinline__ Units units_of(const LayerParams& p, int tokens, bool routed) {
+  const int closed = tokens / kQuantGroup, open = tokens % kQuantGroup > 0;
+  Units u{0, 0, closed, closed, closed + open};
+  if (routed && tokens) {  // nothing was evicted: the query is at position tokens - 1
+    const int first = max(0, (tokens - 1) / p.C - p.local);
     u.a_end = min(p.sink, first) * p.Ng;
     u.b_base = first * p.Ng;
-    u.fixed = u.a_end + it.closed - u.b_base;
+    u.fixed = u.a_end + closed - u.b_base;
     u.groups = u.fixed + p.kg;
-    u.total = u.groups + (it.rest > 0);
+    u.total = u.groups + open;
   }
   return u;
 }
 
 // Scratch of one call.
 struct Workspace {
-  int2* parts;     // [items]: first warp of the item, number of warps
+  int2* parts;     // [items]: first warp of the item, number of warps (0: no tokens)
   float* stat;     // [warps + items][16][4]: weight reference less the score's, score reference, denominator
   float* sum;      // [warps + items][G][D], dimensions in the kernel's order
+  int warps;       // at most
   float2* group;   // [items][G][max_groups + kg]: each unit's sum (-1: a routed id that is not
                    // kept) and its reference, in the virtual list's order (weights only)
 };
@@ -543,7 +545,7 @@ struct Warp {
 template <typename T, int D, int FORMAT, int GM>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(GM))
 quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                    LayerParams p, QuantCache qc, const T* q, const int64_t* __restrict__ pos,
+                    LayerParams p, QuantCache qc, const T* q, const int64_t* pos,
                     const int32_t* group_idx, Workspace ws, unsigned* err) {
   using W = Warp<T, D, FORMAT, GM>;
   constexpr int NT = W::NT, NK = W::NK;
@@ -557,6 +559,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   __shared__ float4 s_units[kWarps][2][32];
   __shared__ int64_t s_before[kThreads];                // list length before each thread's rows
   __shared__ int64_t s_all;
+  __shared__ int s_tokens[kThreads];                    // live tokens of each thread's row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   uint8_t* ring = s_rings + warp * kRing;
   const uint32_t ring_at = ptx::smem_u32(ring);
@@ -569,34 +572,54 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     ptx::prefetch_tensormap(&map_k);
     ptx::prefetch_tensormap(&map_v);
   }
-  // What kernels of this library write is read, and the scratch that the merge of
-  // an earlier call may still read is written, behind pdl_wait: the counts of
-  // evicted groups first of all.  Only positions come before it (a query may be
-  // another call's output).
-  bool waited = qc.evicted != nullptr;
-  if (waited) pdl_wait();
-
   auto worker = [&]() { return static_cast<int64_t>(blockIdx.x) * kWarps + warp; };
-  auto slice_length = [&](int64_t all) {
-    const int64_t slices = static_cast<int64_t>(gridDim.x) * kWarps;
-    return max(static_cast<int64_t>(kMinSlice), (all + slices - 1) / slices);
-  };
   // The list's rows are the sequences, whose `same` KV heads have equal lengths, or,
-  // where eviction may have made them differ, the items.  An item's length in the
-  // list: its units, its fixed work in front.
+  // where eviction may have made them differ, the items.
   const int same = qc.evicted ? 1 : p.Hkv, rows = qc.evicted ? items : p.B;
-  auto item_length = [&](int row, unsigned* e) {
-    const int64_t pb = pos[qc.evicted ? row / p.Hkv : row];
-    const int n = units_of(p, quant_item(qc, pb, row, e), pb, group_idx != nullptr).total;
-    return n ? n + kItemCost : 0;
+  auto tokens_of = [&](int row, unsigned* e) { return quant_item(qc, pos[qc.evicted ? row / p.Hkv : row], row, e).tokens(); };
+  // A row's items' length in the list: their units, their fixed work in front.
+  auto length_of = [&](int tokens) { return tokens ? units_of(p, tokens, group_idx != nullptr).total + kItemCost : 0; };
+  const int per = (rows + kThreads - 1) / kThreads;  // rows a thread sums up
+  // Every input may be what the kernel just before writes, positions and counts of
+  // evicted groups too, and the scratch may still be read by an earlier call's merge: all
+  // of it is used behind pdl_wait.  Where a thread has one row at most, the search for the
+  // slice goes ahead of the wait by the positions that stand there then, and is done
+  // again if behind it one has changed (calls back to back, 4 short float32 sequences: 11.8 us
+  // with the search behind the wait, 10.2 so; a 1K prompt 10.0 and 9.0).
+  bool waited = per > 1 || qc.evicted;
+  if (waited) pdl_wait();
+  // Where there are more rows, positions are read again below.  They do not change while a
+  // call runs; if they do, its result is undefined, but every index stays in range and
+  // the loops end: the two that look for items at the last one.
+  int item;
+  int skip;   // of the item's length, where the slice enters it
+  int left;   // of the slice (at most the longest item's length, or a 1000th of the list)
+  int slice;  // a whole one's length
+  int b, h, tokens, u_lo, u_hi;  // of the item; the slice has its units [u_lo, u_hi)
+  Units un;
+  auto enter_item = [&]() {
+    b = item / p.Hkv;
+    h = item % p.Hkv;
+    const int row = qc.evicted ? item : b;
+    tokens = per == 1 ? s_tokens[row] : tokens_of(row, nullptr);
+    un = units_of(p, tokens, group_idx != nullptr);
+    u_lo = max(skip - kItemCost, 0);
+    u_hi = min(skip + left - kItemCost, un.total);
   };
-  // where this warp's slice [lo, hi) of the list begins
-  const int per = (rows + kThreads - 1) / kThreads;
-  {
-    int64_t mine = 0;
-    for (int i = min(rows, tid * per); i < min(rows, (tid + 1) * per); ++i)
-      mine += static_cast<int64_t>(item_length(i, blockIdx.x == 0 ? err : nullptr)) * same;
+  for (;;) {
+    int tokens = 0;
+    int64_t mine = 0, seen = 0;
+    if (!waited) {  // past L1, which must not keep what stands there now
+      seen = tid < rows ? __ldcg(pos + tid) : -1;
+      tokens = quant_item(qc, seen, tid, nullptr).tokens();
+      mine = static_cast<int64_t>(length_of(tokens)) * same;
+    }
+    for (int i = min(rows, tid * per); waited && i < min(rows, (tid + 1) * per); ++i) {
+      tokens = tokens_of(i, blockIdx.x == 0 ? err : nullptr);
+      mine += static_cast<int64_t>(length_of(tokens)) * same;
+    }
     s_before[tid] = mine;
+    s_tokens[tid] = tokens;
     __syncthreads();
     if (warp == 0) {
       int64_t v[kWarps], sum = 0;
@@ -620,68 +643,80 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       if (lane == 31) s_all = x;
     }
     __syncthreads();
-  }
-  int item;
-  int skip;   // of the item's length, where the slice enters it
-  int left;   // of the slice (at most the longest item's length, or a 1000th of the list)
-  {
-    const int64_t all = s_all, slice = slice_length(all);
-    const int64_t lo = slice * worker();
-    if (lo >= all) {
-      if (!waited) pdl_wait();  // a grid ends after the one before it, even if it has no work
-      return;
-    }
-    left = static_cast<int>(min(slice, all - lo));
-    int owner = -1;  // the last thread whose rows begin at or before lo
+    const int64_t all = s_all, slices = static_cast<int64_t>(gridDim.x) * kWarps;
+    slice = max(kMinSlice, static_cast<int>((all + slices - 1) / slices));
+    const int64_t lo = slice * worker();  // the slice is [lo, lo + left) of the list
+    left = static_cast<int>(min(static_cast<int64_t>(slice), max(all - lo, static_cast<int64_t>(0))));
+    item = 0;
+    skip = 0;
+    if (left > 0) {
+      int owner = -1;  // the last thread whose rows begin at or before lo
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) owner += __popc(__ballot_sync(0xffffffffu, s_before[j * 32 + lane] <= lo));
-    int64_t start = s_before[owner];  // where the row begins in the list
-    for (int row = owner * per;; row += 32) {
-      const int n = row + lane < rows ? item_length(row + lane, nullptr) : 0;
-      int64_t x = static_cast<int64_t>(n) * same;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const unsigned beyond = __ballot_sync(0xffffffffu, start + x > lo);
-      if (beyond) {
-        const int j = __ffs(beyond) - 1, length = __shfl_sync(0xffffffffu, n, j);
-        start += __shfl_sync(0xffffffffu, x - static_cast<int64_t>(n) * same, j);
+      for (int j = 0; j < kWarps; ++j) owner += __popc(__ballot_sync(0xffffffffu, s_before[j * 32 + lane] <= lo));
+      int64_t start = s_before[owner];  // where the row begins in the list
+      auto enter = [&](int row, int length) {
         const int head = static_cast<int>(static_cast<uint64_t>(lo - start) / static_cast<uint32_t>(length));
-        item = (row + j) * same + head;
+        item = row * same + head;
         skip = static_cast<int>(lo - start - static_cast<int64_t>(head) * length);
-        break;
+      };
+      if (per == 1) {  // its row is not empty: the next one would begin where it does
+        enter(owner, length_of(s_tokens[owner]));
+      } else {
+        item = items;
+        for (int row = owner * per; row < rows; row += 32) {
+          const int n = row + lane < rows ? length_of(tokens_of(row + lane, nullptr)) : 0;
+          int64_t x = static_cast<int64_t>(n) * same;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          const unsigned beyond = __ballot_sync(0xffffffffu, start + x > lo);
+          if (beyond) {
+            const int j = __ffs(beyond) - 1, length = __shfl_sync(0xffffffffu, n, j);
+            start += __shfl_sync(0xffffffffu, x - static_cast<int64_t>(n) * same, j);
+            enter(row + j, length);
+            break;
+          }
+          start += __shfl_sync(0xffffffffu, x, 31);
+        }
       }
-      start += __shfl_sync(0xffffffffu, x, 31);
+      if (item < items) enter_item();
     }
+    if (waited) break;
+    pdl_wait();
+    waited = true;
+    if (!__syncthreads_or(tid < rows && pos[tid] != seen)) {
+      if (blockIdx.x == 0 && tid < rows) tokens_of(tid, err);  // flags what is wrong
+      break;
+    }
+  }
+  if (blockIdx.x == 0) {  // items without units have no partials
+    for (int i = min(rows, tid * per); i < min(rows, (tid + 1) * per); ++i)
+      if ((per == 1 ? s_tokens[i] : tokens_of(i, nullptr)) == 0)
+        for (int k = 0; k < same; ++k) ws.parts[static_cast<int64_t>(i) * same + k] = make_int2(0, 0);
   }
 
   W w;
   int stage = 0;       // of the ring, and its phase
   uint32_t phase = 0;
   bool alive = true;   // no wait gave up
-  for (; left > 0; ++item) {
-    const int b = item / p.Hkv, h = item % p.Hkv;
-    const int64_t pb = pos[b];
-    const QuantItem it = quant_item(qc, pb, item, nullptr);
-    const Units un = units_of(p, it, pb, group_idx != nullptr);
+  for (bool entered = true; left > 0; ++item, entered = false) {
+    if (item >= items) {
+      flag_error(err, kErrPos);
+      break;
+    }
+    if (!entered) enter_item();
     if (un.total == 0) continue;
-    const int u_lo = max(skip - kItemCost, 0);
-    const int u_hi = min(skip + left - kItemCost, un.total);
     if (u_hi <= 0) break;  // only the item's fixed part
     left -= un.total + kItemCost - skip;
     skip = 0;
-    if (!waited) {
-      pdl_wait();
-      waited = true;
-    }
     typename W::Row q_raw[NT][NK];
     w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
     pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
     if (lane == 0 && u_lo == 0) {  // this warp has the item's first unit; its last one is total - u_hi further on
-      const int64_t slice = slice_length(s_all);
-      ws.parts[item] = make_int2(static_cast<int>(worker()), static_cast<int>((max(0, -left) + slice - 1) / slice) + 1);
+      const int me = static_cast<int>(worker()), more = static_cast<int>((static_cast<unsigned>(max(0, -left)) + slice - 1) / slice);
+      ws.parts[item] = make_int2(me, min(more, static_cast<int>(gridDim.x) * kWarps - 1 - me) + 1);
     }
     if (un.groups > un.fixed) {
       // kept: ids of candidate chunks, larger than all candidate ids before them
@@ -771,7 +806,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     w.clear();
     if (u_hi > un.groups) {
       const int64_t at = static_cast<int64_t>(item) * kQuantGroup * D;
-      w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, it.rest, group,
+      w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, tokens % kQuantGroup, group,
              stride, un.groups, p.G);
     }
     stage_scales();
@@ -901,7 +936,7 @@ constexpr int kMergeEntries = 1024;
 constexpr int merge_warps(int split) { return split > 1 ? split : 8; }
 template <int D, typename TO, int SPLIT>
 __global__ void __launch_bounds__(merge_warps(SPLIT) * 32)
-quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos, Workspace ws,
+quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* pos, Workspace ws,
                    const int32_t* group_idx, const float* weight_in,
                    float* weight_out, TO* __restrict__ out,
                    float* __restrict__ lse) {
@@ -914,13 +949,12 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv), h = static_cast<int>(item % p.Hkv);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t pb = pos[b];
   pdl_wait();
   pdl_trigger();
-  const int2 found = ws.parts[item];  // written if the item has units
-  const QuantItem it = quant_item(qc, pb, item, nullptr);
-  const int units = it.units();
-  const int2 parts = units ? found : make_int2(0, 0);
+  const int2 found = ws.parts[item];
+  // only partials that exist, whatever the words hold
+  const bool there = found.x >= 0 && found.y > 0 && found.y <= ws.warps - found.x;
+  const int2 parts = there ? found : make_int2(0, 0);
   const int64_t first = parts.x + item;
   const float4* stat = reinterpret_cast<const float4*>(ws.stat) + first * 16;
   const int head_blocks = (p.G + kHeads - 1) / kHeads;
@@ -1003,6 +1037,8 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
     }
   } else {
     const int e0 = (static_cast<int>(blockIdx.y) - head_blocks) * kMergeEntries;
+    const QuantItem it = quant_item(qc, pos[b], item, nullptr);
+    const int units = it.units();
     if (e0 < units) {
       for (int head = warp; head < p.G; head += kMergeWarps) {
         float rs = kNoRef, l = 0.f;
@@ -1019,7 +1055,7 @@ quant_merge_kernel(LayerParams p, QuantCache qc, const int64_t* __restrict__ pos
         }
       }
       __syncthreads();
-      const Units un = units_of(p, it, pb, group_idx != nullptr);
+      const Units un = units_of(p, it.tokens(), group_idx != nullptr);
       const int stride = qc.max_groups + p.kg;
       auto unit_weight = [&](int u) {
         float sum = 0.f;
@@ -1060,7 +1096,8 @@ int heads_rounded(const LayerParams& p) { return p.G <= 4 ? 4 : p.G <= 8 ? 8 : 1
 // Scratch layout; base may be null (sizes only).
 size_t layout(const LayerParams& p, int max_groups, bool weight, char* base, Workspace* ws) {
   const size_t items = static_cast<size_t>(p.B) * p.Hkv;
-  const size_t parts = items + static_cast<size_t>(device_sm_count()) * ctas_per_sm(heads_rounded(p)) * kWarps;
+  ws->warps = device_sm_count() * ctas_per_sm(heads_rounded(p)) * kWarps;
+  const size_t parts = items + ws->warps;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* x = base + at;

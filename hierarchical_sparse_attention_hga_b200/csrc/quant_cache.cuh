@@ -41,6 +41,7 @@ struct QuantItem {
   int rest;    // rows of the open group (0..15)
   bool ok;     // false: the position or the count of evicted groups was bad
   __device__ __forceinline__ int units() const { return closed + (rest > 0); }
+  __device__ __forceinline__ int tokens() const { return closed * kQuantGroup + rest; }
 };
 
 // The item's state at position pos (of its last token; -1: empty).  A position

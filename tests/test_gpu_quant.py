@@ -773,3 +773,95 @@ def test_attend_scores_far_beyond_one_another(dtype, fmt, product, sign):
                 assert (np.abs(out[b, rows, 0] - want) <= tol).all(), (b, h, at)
                 assert (np.abs(lse[b, rows, 0] - want_lse) <= (136 + 2) * 2.0 ** -22 * np.abs(want_lse)).all()
                 np.testing.assert_allclose(w_out[b, h, :len(weight)], weight, rtol=2.0 ** -20, atol=0)
+
+
+# ---- inputs that the kernel just before writes
+
+
+class Late:
+    """An input that hga_quant_evict, as a copier of 32-bit words, writes just before the call that
+    reads it: that kernel releases its dependents before it has written anything, so a call that
+    reads ahead of it finds what stood there before."""
+
+    WORDS = 49152
+
+    def __init__(self, right, stale):
+        self.layer = B.Layer(batch=1, heads_q=1, heads_kv=1, head_dim=64)
+        words = [t.contiguous().view(torch.int32).flatten() for t in (right, stale)]
+        n = -(-words[0].numel() // 4) * 4
+        assert n < self.WORDS
+        self.src, self.old, self.dst = torch.zeros(3, self.WORDS, dtype=torch.int32, device="cuda")
+        for buf, x in ((self.src, words[0]), (self.old, words[1])):
+            buf[-n:][:x.numel()] = x
+        self.tensor = self.dst[-n:][:words[0].numel()].view(right.dtype).view(right.shape)
+        self.pos = torch.tensor([-1], device="cuda")
+        self.weight = torch.zeros(2, self.WORDS, device="cuda")
+        self.gone = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+        self.cache = B.quant_cache(None, None, None, None, None, None, self.src, 1, self.WORDS)
+
+    def reset(self):
+        self.dst.copy_(self.old)
+
+    def write(self):
+        B.hga_quant_evict(self.layer, self.cache, self.pos, 1, 0, 0, self.weight[0], self.weight[1], self.dst, self.gone)
+
+
+def check_late(state, inputs, call):
+    """call(inputs) -> leaves its results in the tensors `state`; each input in turn is written by
+    the kernel before the call, over stale contents of the same type."""
+    before = [t.clone() for t in state]
+
+    def results(first, given):
+        for t, x in zip(state, before):
+            t.copy_(x)
+        torch.cuda.synchronize()
+        first()
+        call(given)
+        torch.cuda.synchronize()
+        assert B.hga_device_status() == 0
+        return [t.clone() for t in state]
+
+    same = {k: right for k, (right, _) in inputs.items()}
+    want = results(lambda: None, same)
+    for name, (right, stale) in inputs.items():
+        late = Late(right, stale)
+        for _ in range(10):
+            late.reset()
+            for t, x in zip(results(late.write, {**same, name: late.tensor}), want):
+                assert torch.equal(t.view(torch.uint8), x.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("batch,evicts,routed", [(6, False, False), (6, True, False), (6, False, True), (150, False, False), (150, False, True)])
+def test_attend_reads_behind_the_kernel_before(batch, evicts, routed):
+    """Few sequences, whose positions are looked at ahead of the wait and again behind it, and
+    more than a CTA has threads."""
+    lens = ([0, 300, 17, 640, 1, 95] * 25)[:batch]
+    layer = dict(topk_groups=8) if routed else {}
+    c = Cache(batch, 2, 64, 41, heads_q=8, seed=32, evicts=evicts, **layer)
+    c.fill(lens)
+    out, lse = torch.empty(batch, 8, 1, 64, device="cuda"), torch.empty(batch, 8, 1, device="cuda")
+    weight = torch.zeros(batch, 2, 41, device="cuda")
+    need = B.hga_quant_attend_workspace_size(c.layer, 41, True)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    q, pos = to_gpu(c.q(), "bf16"), c.pos_t()
+    stale = torch.tensor(([5, 30, 600, -1, 639, 80] * 25)[:batch], device="cuda")
+    inputs = {"pos": (pos, stale), "weight": (torch.rand_like(weight), torch.full_like(weight, 9.0))}
+    if batch == 6:
+        inputs["q"] = (q, torch.full_like(q, float("nan")))
+    if evicts:
+        inputs["evicted"] = (c.evicted, c.evicted + torch.tensor([0, 5, 1, 20, 0, 2], device="cuda", dtype=torch.int32)[:, None])
+    if routed:
+        idx = torch.full((batch, 2, 8), -1, dtype=torch.int32)
+        for b, n in enumerate(lens):
+            for h in range(2):
+                ids = routed_ids(c.rng, n, 8, 64, 1, 4)
+                idx[b, h, :len(ids)] = torch.tensor(ids, dtype=torch.int32)
+        inputs["group_idx"] = (idx.cuda(), torch.full_like(idx.cuda(), -1))
+
+    def call(x):
+        view = c.view()
+        if evicts:
+            view.evicted = x["evicted"].data_ptr()
+        B.hga_quant_attend(c.layer, view, x.get("q", q), x["pos"], out, lse, x.get("group_idx"), x["weight"], weight, ws, need)
+
+    check_late([out, lse, weight], inputs, call)
