@@ -70,7 +70,7 @@ size_t smem_bytes(int max_groups, int rows) {
 // ROWS: rows in shared memory at a time (the weights, or the weights and the table).
 template <int NT, int ROWS>
 __global__ void __launch_bounds__(NT)
-quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* __restrict__ pos, int keep, int sink,
+quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* pos, int keep, int sink,
                    int recent, const float* weight_in, float* weight_out, int32_t* table_out,
                    int32_t* evicted_out, unsigned* err) {
   extern __shared__ __align__(16) uint32_t s_mem[];
@@ -90,10 +90,10 @@ quant_evict_kernel(int Hkv, QuantCache qc, const int64_t* __restrict__ pos, int 
   float* w_out = weight_out + item * max_groups;
   const int32_t* t_in = qc.table + item * max_groups;
   int32_t* t_out = table_out + item * max_groups;
-  const int64_t pb = pos[item / Hkv];
-  pdl_wait();
+  pdl_wait();  // the position too may be what the kernel just before writes
   pdl_trigger();  // dependents wait for the whole grid; they may be launched as its CTAs leave
 
+  const int64_t pb = pos[item / Hkv];
   const int gone = qc.evicted ? qc.evicted[item] : 0;  // on its way with the rows
 #pragma unroll 4
   for (int i = tid; i < max_groups; i += NT) {

@@ -865,3 +865,19 @@ def test_attend_reads_behind_the_kernel_before(batch, evicts, routed):
         B.hga_quant_attend(c.layer, view, x.get("q", q), x["pos"], out, lse, x.get("group_idx"), x["weight"], weight, ws, need)
 
     check_late([out, lse, weight], inputs, call)
+
+
+@pytest.mark.parametrize("max_groups", [40, 30000])
+def test_evict_reads_behind_the_kernel_before(max_groups):
+    c = Cache(1, 1, 64, max_groups, seed=33, evicts=True)
+    c.pos[:] = 16 * (max_groups - 2) + 2
+    w = torch.rand(1, 1, max_groups, device="cuda")
+    outs = [torch.empty_like(w), torch.empty_like(c.table), torch.empty_like(c.evicted)]
+    inputs = {"pos": (c.pos_t(), torch.tensor([16 * 5 - 1], device="cuda")), "weight": (w, torch.zeros_like(w)),
+              "table": (c.table, torch.zeros_like(c.table)), "evicted": (c.evicted, c.evicted + 7)}
+
+    def call(x):
+        view = B.quant_cache(None, None, None, None, None, None, x["table"], c.n_slots, max_groups, evicted=x["evicted"])
+        B.hga_quant_evict(c.layer, view, x["pos"], 11, 1, 2, x["weight"], *outs)
+
+    check_late(outs, inputs, call)
