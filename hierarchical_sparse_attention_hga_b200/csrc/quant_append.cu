@@ -204,10 +204,9 @@ __device__ __forceinline__ void write_group(const Piece<T, D / 32> (&x)[kGroup],
 
 template <typename T, int D, int FORMAT, int NG>
 __global__ void __launch_bounds__(32 * NG, ctas_per_sm(NG))
-quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
-                    const T* __restrict__ v_new, int n_new, const int32_t* __restrict__ counts,
-                    const int64_t* __restrict__ pos, float* __restrict__ chunk_sum,
-                    float* __restrict__ group_sum, unsigned* err) {
+quant_append_kernel(LayerParams p, QuantCache qc, const T* k_new, const T* v_new, int n_new,
+                    const int32_t* counts, const int64_t* pos, float* chunk_sum, float* group_sum,
+                    unsigned* err) {
   constexpr int P = D / 2, E = D / 32, H = E / 2;  // H: pairs of a lane
   __shared__ float s_gsum[2][NG][D];  // raw group sums of a chunk, by turns
   // rotations of a group's tokens (cosines, then sines, of H pairs at a time) and of a chunk's groups
@@ -217,6 +216,8 @@ quant_append_kernel(LayerParams p, QuantCache qc, const T* __restrict__ k_new,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t item = blockIdx.x;
   const int b = static_cast<int>(item / p.Hkv);
+  // No input is const __restrict__: the kernel just before may still write it while this
+  // one runs, so it may not be loaded as data that nobody writes.
   pdl_wait();
   pdl_trigger();  // dependents wait for the whole grid; they may be launched as its CTAs leave
 

@@ -42,11 +42,10 @@
  *    C).
  *  - A call's kernels may start while a kernel before them in the stream still
  *    runs, if that one releases its dependents early (programmatic dependent
- *    launch, as this library's own kernels do).  hga_quant_attend and
- *    hga_quant_evict use nothing from before that kernel has finished.  Other
- *    calls may read pos, q, k and v earlier: a kernel that releases its
- *    dependents before it has written them may not stand directly before such
- *    a call.
+ *    launch, as this library's own kernels do).  The hga_quant_* calls use
+ *    nothing from before that kernel has finished.  Other calls may read pos, q,
+ *    k and v earlier: a kernel that releases its dependents before it has
+ *    written them may not stand directly before such a call.
  */
 #ifndef HGA_H_
 #define HGA_H_

@@ -881,3 +881,20 @@ def test_evict_reads_behind_the_kernel_before(max_groups):
         B.hga_quant_evict(c.layer, view, x["pos"], 11, 1, 2, x["weight"], *outs)
 
     check_late(outs, inputs, call)
+
+
+@pytest.mark.parametrize("dtype,fmt,n", [("bf16", "e4m3", 1), ("bf16", "int8", 37), ("f32", "e4m3", 20)])
+def test_append_reads_behind_the_kernel_before(dtype, fmt, n):
+    c = Cache(4, 2, 64, 12, dtype, fmt, seed=34)
+    c.fill([15, 0, 90, 31])
+    cs, gs = torch.zeros(4, 2, 3, 64, device="cuda"), torch.rand(4, 2, 12, 64, device="cuda")
+    k, v = (to_gpu(c.rng.standard_normal((4, 2, n, 64)), dtype) for _ in "kv")
+    counts = torch.tensor([n, n // 2, n, 1], dtype=torch.int32, device="cuda")
+    pos = c.pos_t() + counts
+    inputs = {"pos": (pos, pos + 16), "counts": (counts, torch.zeros_like(counts)),
+              "k": (k, torch.full_like(k, float("nan"))), "v": (v, torch.full_like(v, float("nan")))}
+
+    def call(x):
+        B.hga_quant_append(c.layer, c.view(), x["k"], x["v"], n, x["pos"], x["counts"], cs, gs)
+
+    check_late([c.k, c.v, c.ks, c.vs, c.kt, c.vt, cs, gs], inputs, call)
