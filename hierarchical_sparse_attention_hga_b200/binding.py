@@ -450,8 +450,8 @@ def hga_quant_append(cfg, cache: HGAQuantCache, k_new, v_new, n_new: int, pos, c
                      chunk_sum=None, group_sum=None, stream=None) -> None:
     """Writes new rows into an 8-bit cache (tail, closed groups, optional summary rows)."""
     _check(load_library().hga_quant_append(ctypes.byref(_cfg(cfg)), ctypes.byref(cache),
-                                           _dense(k_new), _dense(v_new), n_new, _ptr(counts),
-                                           _ptr(pos), _ptr(chunk_sum), _ptr(group_sum),
+                                           _dense(k_new), _dense(v_new), n_new, _dense(counts),
+                                           _dense(pos), _dense(chunk_sum), _dense(group_sum),
                                            _stream(stream)), "hga_quant_append")
 
 
@@ -469,18 +469,18 @@ def hga_quant_attend(cfg, cache: HGAQuantCache, q, pos, out, lse=None, group_idx
     """Decode attention over an 8-bit cache: every live group, or the routed sets of group_idx;
     weight_out = weight_in + each group's attention weight."""
     _check(load_library().hga_quant_attend(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _dense(q),
-                                           _ptr(pos), _ptr(group_idx), _ptr(weight_in),
-                                           _ptr(weight_out), _dense(out), _ptr(lse),
-                                           _ptr(workspace), workspace_bytes, _stream(stream)),
+                                           _dense(pos), _dense(group_idx), _dense(weight_in),
+                                           _dense(weight_out), _dense(out), _dense(lse),
+                                           _dense(workspace), workspace_bytes, _stream(stream)),
            "hga_quant_attend")
 
 
 def hga_quant_evict(cfg, cache: HGAQuantCache, pos, keep: int, sink: int, recent: int, weight_in,
                     weight_out, table_out, evicted_out, stream=None) -> None:
     """Keeps the sinks, the newest groups and the heaviest of the others, `keep` in all."""
-    _check(load_library().hga_quant_evict(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _ptr(pos),
-                                          keep, sink, recent, _ptr(weight_in), _ptr(weight_out),
-                                          _ptr(table_out), _ptr(evicted_out), _stream(stream)),
+    _check(load_library().hga_quant_evict(ctypes.byref(_cfg(cfg)), ctypes.byref(cache), _dense(pos),
+                                          keep, sink, recent, _dense(weight_in), _dense(weight_out),
+                                          _dense(table_out), _dense(evicted_out), _stream(stream)),
            "hga_quant_evict")
 
 

@@ -210,3 +210,40 @@ def test_slices_of_larger_tensors_are_refused():
     for q, out in ((part, whole), (whole, part)):
         with pytest.raises(ValueError):
             B.hga_quant_attend(layer, cache(), q, 16, out, stream=0)
+
+
+def strided(*shape, dtype=torch.float32):
+    """Tensors of this shape that are not contiguous: every other element, and one row for all."""
+    yield torch.zeros(*shape, 2, dtype=dtype)[..., 0]
+    if shape[0] > 1:
+        yield torch.zeros(1, *shape[1:], dtype=dtype).expand(*shape)
+
+
+@pytest.mark.parametrize("name", ["pos", "counts", "chunk_sum", "group_sum"])
+def test_append_refuses_strided(name):
+    shape = {"pos": (2,), "counts": (2,)}.get(name, (2, 2, 4, 128))
+    for bad in strided(*shape, dtype={"pos": torch.int64, "counts": torch.int32}.get(name, torch.float32)):
+        args = {"pos": 16, "counts": 16, "chunk_sum": 16, "group_sum": 16, name: bad}
+        with pytest.raises(ValueError):
+            B.hga_quant_append(B.Layer(**LAYER), cache(), 16, 16, 1, stream=0, **args)
+
+
+@pytest.mark.parametrize("name", ["pos", "lse", "group_idx", "weight_in", "weight_out", "workspace"])
+def test_attend_refuses_strided(name):
+    shape = {"pos": (2,), "lse": (2, 8, 1), "group_idx": (2, 2, 32), "workspace": (4096,)}.get(name, (2, 2, 4))
+    kind = {"pos": torch.int64, "group_idx": torch.int32, "workspace": torch.uint8}.get(name, torch.float32)
+    for bad in strided(*shape, dtype=kind):
+        args = {"pos": 16, "lse": 16, "group_idx": 16, "weight_in": 16, "weight_out": 16, "workspace": 16, name: bad}
+        with pytest.raises(ValueError):
+            B.hga_quant_attend(B.Layer(**LAYER), cache(), 16, args.pop("pos"), 16, workspace_bytes=1 << 40,
+                               stream=0, **args)
+
+
+@pytest.mark.parametrize("name", ["pos", "weight_in", "weight_out", "table_out", "evicted_out"])
+def test_evict_refuses_strided(name):
+    shape = {"pos": (2,), "evicted_out": (2, 2)}.get(name, (2, 2, 4))
+    kind = {"pos": torch.int64, "evicted_out": torch.int32, "table_out": torch.int32}.get(name, torch.float32)
+    for bad in strided(*shape, dtype=kind):
+        args = {"pos": 16, "weight_in": 16, "weight_out": 16, "table_out": 16, "evicted_out": 16, name: bad}
+        with pytest.raises(ValueError):
+            B.hga_quant_evict(B.Layer(**LAYER), cache(), args.pop("pos"), 4, 1, 1, stream=0, **args)
