@@ -63,6 +63,10 @@ __host__ __device__ __forceinline__ int64_t paged_row(const KvPages& kv, int Hkv
 // runs out (nothing is in flight into that stage) and the kernel reports
 // HGA_ERR_TIMEOUT through the device error word.
 constexpr unsigned kDebugSkipRouteArrive = 1u;
+// Test hook of hga_quant_attend: the warp with the first units of the first
+// (sequence, KV head) withholds its first copies, whose barrier then never
+// completes, and its wait gives up.
+constexpr unsigned kDebugSkipQuantCopy = 2u;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

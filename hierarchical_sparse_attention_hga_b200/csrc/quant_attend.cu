@@ -701,6 +701,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   int stage = 0;       // of the ring, and its phase
   uint32_t phase = 0;
   bool alive = true;   // no wait gave up
+  const uint64_t limit_ns = p.debug & kDebugSkipQuantCopy ? 2000000ull : 50000000ull;
   for (bool entered = true; left > 0; ++item, entered = false) {
     if (item >= items) {
       flag_error(err, kErrPos);
@@ -785,11 +786,12 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
           staged = issued;
         }
         uint8_t* dst = ring + stage * kTile * kUnitBytes;
-        if (lane == 0) ptx::mbar_expect_tx(&s_full[warp][stage], kTile * kUnitBytes);
+        const bool copies = lane == 0 && !((p.debug & kDebugSkipQuantCopy) && item == 0 && u_lo == 0 && issued == 0);
+        if (copies) ptx::mbar_expect_tx(&s_full[warp][stage], kTile * kUnitBytes);
 #pragma unroll
         for (int j = 0; j < kTile; ++j) {
           const int slot = __shfl_sync(0xffffffffu, slots, (issued & 31) + j);
-          if (lane == 0) {  // a row before the first reads as zeros
+          if (copies) {  // a row before the first reads as zeros
             const int row = slot >= 0 ? slot * kQuantGroup : -kQuantGroup;
             ptx::tma_load_2d(dst + j * kUnitBytes, &map_k, &s_full[warp][stage], 0, row);
             ptx::tma_load_2d(dst + j * kUnitBytes + kUnitBytes / 2, &map_v, &s_full[warp][stage], 0, row);
@@ -799,23 +801,30 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
     };
 
-    int u = u_lo;
+    if (alive) {
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) issue((stage + k) % kStages);
+      for (int k = 0; k < kStages; ++k) issue((stage + k) % kStages);
+    }
     w.load_q(q_raw);
     w.clear();
-    if (u_hi > un.groups) {
+    if (u_hi > un.groups && alive) {
       const int64_t at = static_cast<int64_t>(item) * kQuantGroup * D;
       w.tail(static_cast<const T*>(qc.k_tail) + at, static_cast<const T*>(qc.v_tail) + at, tokens % kQuantGroup, group,
              stride, un.groups, p.G);
     }
     stage_scales();
     __syncwarp();
-    for (; u < g_hi; u += kTile) {
-      // after a wait gave up, the others are short; every copy is still waited for
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait_ns(&s_full[warp][stage], phase, kWaitLimit, alive ? 50000000ull : 1000000ull))) {
+    for (int u = u_lo; u < g_hi && alive; u += kTile) {
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_ns(&s_full[warp][stage], phase, kWaitLimit, limit_ns))) {
+        // the warp starts no more copies; those under way, this stage's and the ones
+        // behind it, get another millisecond each before it goes on
         alive = false;
         flag_error(err, kErrTimeout);
+#pragma unroll 1
+        for (int k = 0; k < kStages && u + k * kTile < u_lo + issued; ++k)
+          ptx::mbar_wait_ns(&s_full[warp][(stage + k) % kStages], stage + k < kStages ? phase : phase ^ 1, kWaitLimit, 1000000ull);
+        __syncwarp();
+        break;
       }
       const uint32_t tile = ring_at + stage * kTile * kUnitBytes;
       float x[kTile][NT][4], mant[kTile], ex[kTile];
@@ -900,8 +909,13 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
     }
 
-    // this slice's partial of the item (empty if a wait gave up)
-    if (!alive) w.clear();
+    // this slice's partial of the item (empty, as are its units' weights, once a wait gave up)
+    if (!alive) {
+      w.clear();
+      if (group)
+        for (int i = u_lo + lane; i < u_hi; i += 32)
+          for (int head = 0; head < p.G; ++head) group[static_cast<int64_t>(head) * stride + i] = make_float2(0.f, kNoRef);
+    }
     const int64_t part = worker() + item;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

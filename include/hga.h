@@ -166,7 +166,10 @@ hga_status hga_device_status(void* stream);
  * copy for the first item of each CTA while the warp still waits for it, so that
  * bounded wait (nothing is in flight into that stage; limited to 2 ms under this
  * flag) runs out; the kernel still reaches every barrier and returns, and
- * hga_device_status() then reports HGA_ERR_TIMEOUT.
+ * hga_device_status() then reports HGA_ERR_TIMEOUT.  Flag 2 makes the warp of
+ * hga_quant_attend that has the first groups of the first (sequence, KV head)
+ * withhold their copies, with the same limit and report: what that warp would
+ * have attended is left out of the result.
  */
 int32_t hga_debug_inject(int32_t flags);
 

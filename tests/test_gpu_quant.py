@@ -898,3 +898,34 @@ def test_append_reads_behind_the_kernel_before(dtype, fmt, n):
         B.hga_quant_append(c.layer, c.view(), x["k"], x["v"], n, x["pos"], x["counts"], cs, gs)
 
     check_late([c.k, c.v, c.ks, c.vs, c.kt, c.vt, cs, gs], inputs, call)
+
+
+# ---- a wait that gives up
+
+
+@pytest.mark.parametrize("lens", [[5000], [60, 33, 200, 0, 47, 90], [700] * 40, [30000] * 4])
+def test_attend_reports_a_copy_that_never_comes(lens):
+    """A warp's first copies are withheld (nothing is in flight into that stage), its wait runs out:
+    the call ends, the status is HGA_ERR_TIMEOUT, what the other warps attend counts, and the next
+    call is right again."""
+    c = Cache(len(lens), 2, 128, -(-max(lens) // 16) + 1, heads_q=8, seed=35)
+    c.fill(lens)
+    q = c.q()
+    w_in = torch.zeros(len(lens), 2, c.max, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    right = c.attend(q, weight=w_in, weight_out=w_out)
+    old = B.hga_debug_inject(2)
+    try:
+        w_bad = torch.full_like(w_in, -5)
+        bad = c.attend(q, weight=w_in, weight_out=w_bad)
+        torch.cuda.synchronize()
+        assert B.hga_device_status() == 5
+    finally:
+        B.hga_debug_inject(old)
+    # the first item's first groups are that warp's
+    assert not w_bad[0, 0, 0].any() and w_out[0, 0, 0] > 0
+    assert torch.isfinite(bad[0]).all() and (w_bad[w_out == -5] == -5).all()
+    if len(lens) > 1:  # the last items are other warps'
+        assert torch.equal(bad[0][-1], right[0][-1]) and torch.equal(w_bad[-1], w_out[-1])
+    w_out.fill_(-5)
+    c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
