@@ -70,7 +70,8 @@ constexpr float kNoRef = -3e38f;     // reference before the first score
 constexpr float kHeadroom = 2.f;     // a raised reference exceeds the maximum by 2 to 3
 constexpr float kWeightExp = 14.f;   // weights are at most 2 * 2^(14 - 2) in f16
 
-// Resident CTAs per SM that the register use allows.
+// Resident CTAs per SM that the register use allows (shared memory may allow fewer:
+// launch_attend).
 __host__ __device__ constexpr int ctas_per_sm(int gm) { return gm == 16 ? 2 : 3; }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -1135,9 +1136,16 @@ cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void
   int64_t most = qc.max_groups;
   if (group_idx) most = std::min(most, (static_cast<int64_t>(p.sink) + p.local + 1) * p.Ng) + p.kg + 1;
   const int64_t slices = (items * (most + kItemCost) + kMinSlice - 1) / kMinSlice;
-  const int64_t resident = static_cast<int64_t>(device_sm_count()) * ctas_per_sm(GM);
-  const unsigned grid = static_cast<unsigned>(std::min((slices + kWarps - 1) / kWarps, resident));
   const size_t smem = 1024 + kWarps * (kStages * kTile * Tile<D>::kUnitBytes + (group_idx ? p.kg * sizeof(int) : 0));
+  // An SM's 228 KB hold fewer CTAs where there are many routed ids (D = 128, from about
+  // 280 on): slices for CTAs that only come in a second wave would be as long as the others.
+  static const size_t fixed = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, quant_attend_kernel<T, D, FORMAT, GM>) == cudaSuccess ? a.sharedSizeBytes : 0;
+  }();
+  const int64_t fits = static_cast<int64_t>(228 * 1024 / (1024 + fixed + smem));
+  const int64_t resident = device_sm_count() * std::min<int64_t>(fits, ctas_per_sm(GM));
+  const unsigned grid = static_cast<unsigned>(std::min((slices + kWarps - 1) / kWarps, resident));
   CUtensorMap map_k, map_v;
   cudaError_t e = make_byte_map(&map_k, qc.k, qc.n_slots * kQuantGroup, D, kQuantGroup);
   if (e == cudaSuccess) e = make_byte_map(&map_v, qc.v, qc.n_slots * kQuantGroup, D, kQuantGroup);

@@ -929,3 +929,41 @@ def test_attend_reports_a_copy_that_never_comes(lens):
         assert torch.equal(bad[0][-1], right[0][-1]) and torch.equal(w_bad[-1], w_out[-1])
     w_out.fill_(-5)
     c.check_attend(q, c.attend(q, weight=w_in, weight_out=w_out), None, w_in, w_out)
+
+
+# ---- many routed groups
+
+
+@pytest.mark.parametrize("dtype,fmt,dim,kg,shared,per_sm", [
+    ("bf16", "e4m3", 128, 32, 4, 3), ("bf16", "int8", 128, 1024, 4, 2), ("f32", "e4m3", 128, 400, 8, 2),
+    ("f32", "int8", 64, 1024, 3, 3), ("bf16", "e4m3", 128, 1024, 16, 2)])
+def test_attend_many_routed_groups(dtype, fmt, dim, kg, shared, per_sm):
+    """Up to 1024 routed groups, which take shared memory from the CTAs: the slices are cut for the
+    warps of the CTAs that an SM holds then (148 SMs), and no warp has one beyond those.  A
+    partial stands at its warp's number plus its item's."""
+    lens = [20011, 333, 19000]
+    c = Cache(3, 2, dim, 1256, dtype, fmt, heads_q=2 * shared, seed=36, topk_groups=kg, sink_chunks=1, local_chunks=4)
+    c.fill(lens)
+    idx = np.full((3, 2, kg), -1, np.int32)
+    entries = []
+    for b, n in enumerate(lens):
+        entries.append([])
+        cur = (n - 1) // 64
+        for h in range(2):
+            ids = routed_ids(c.rng, n, kg, 64, 1, 4)
+            idx[b, h, :len(ids)] = ids
+            chosen = set(ids)
+            entries[b].append([g for g in range(n // 16) if g // 4 < 1 or g // 4 >= cur - 4 or g in chosen])
+    q = c.q()
+    w_in = torch.rand(3, 2, 1256, device="cuda")
+    w_out = torch.full_like(w_in, -5)
+    need = B.hga_quant_attend_workspace_size(c.layer, c.max, True)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = c.attend(q, torch.tensor(idx).cuda(), weight=w_in, weight_out=w_out, ws=ws)
+    c.check_attend(q, got, entries, w_in, w_out)
+    warps = 4 * per_sm * torch.cuda.get_device_properties(0).multi_processor_count
+    most = 4 * (2 if shared > 8 else 3) * torch.cuda.get_device_properties(0).multi_processor_count
+    last = int((ws[:(most + 6) * 256].view(-1, 256)[:, :16] != 0xFF).any(1).nonzero().max())
+    assert last - 5 < warps
+    if kg >= 400:  # long enough for a slice for most of them
+        assert last - 5 >= warps // 2
