@@ -24,12 +24,17 @@
 // and of O's rows; they are chosen so that a lane's bytes are consecutive ones of
 // a row and no two lanes of a phase meet in a bank (see Tile).
 //
-// Precision.  bf16 queries, scaled by a power of two, are exact in f16; float32
-// ones are split into a high and a low half.  The softmax weights, multiplied by
-// v_scale, are split into two halves as well (22 bits): with at most four heads
-// the low halves take the unused four columns, for free.  References of the
-// running softmax are integers, so every rescaling is exact, and v_scale enters
-// as exponent and mantissa, so its size never costs bits.  A weight's reference
+// Precision.  f16 operands hold the codes exactly.  bf16 queries and tails are scaled by
+// a power of two (a query's and a tail's own) and exact down to 2^-31 of their largest element;
+// float32 ones are split into a high and a low half, 22 bits, without the product of the two
+// low halves; either way no element is off by more than 2^-39 of the largest, where
+// f16 ends.  The softmax weights, multiplied by v_scale, are split likewise: 22 bits of a
+// weight down to 2^-14 of the largest p v_scale that the warp has met, below that an error of
+// up to 2^-36 of that largest one (so a dimension that only such light groups feed has
+// fewer bits than float32 would leave it; the row has not).  With at most four heads the
+// low halves take the unused four columns, for free.  Exponentials are ex2.approx (2 ulp).
+// References of the running softmax are integers, so every rescaling is exact, and v_scale
+// enters as exponent and mantissa, so its size never costs bits.  A weight's reference
 // (of p v_scale) is kept as its distance from the score's, and the exponents of
 // weights are sums of distances: beyond 2^24 a score has no bits left to which an
 // exponent could be added.  Each tile's product starts from zero and is added to the
@@ -68,7 +73,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kWaitLimit = 1u << 26;  // bounded mbarrier polls (and 50 ms)
 constexpr float kNoRef = -3e38f;     // reference before the first score
 constexpr float kHeadroom = 2.f;     // a raised reference exceeds the maximum by 2 to 3
-constexpr float kWeightExp = 14.f;   // weights are at most 2 * 2^(14 - 2) in f16
+constexpr float kWeightExp = 14.f;   // weights are below 2 * 2^14 in f16 (65504), one of them at least 2^11
 
 // Resident CTAs per SM that the register use allows (shared memory may allow fewer:
 // launch_attend).

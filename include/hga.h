@@ -631,9 +631,14 @@ hga_status hga_quant_append(const hga_config* cfg, const hga_quant_cache* cache,
  * A query that holds an infinity or NaN makes its head's outputs NaN; so do, for
  * every head, an attended group that held one and a tail that holds one.
  * A sequence with no tokens gets zeros and an LSE of -inf.  A bad position, table
- * entry or group id is flagged and skipped as in hga_attend.  Sums are float32;
- * the softmax weights enter the products with 22 bits, the codes exactly.  The
- * result does not depend on scheduling.
+ * entry or group id is flagged and skipped as in hga_attend.  The result does
+ * not depend on scheduling.
+ * Precision: sums are float32.  The products take the codes exactly; softmax
+ * weights, times v_scale, with 22 bits, or to 2^-36 of the (sequence, KV
+ * head)'s largest where that is coarser; queries and tail rows with 22 bits, or to
+ * 2^-39 of the query's or the tail's largest element.  So an output dimension
+ * that only tokens of little weight feed, and tail rows far smaller than others
+ * of the same tail, keep fewer bits than float32 arithmetic would leave them.
  */
 hga_status hga_quant_attend_workspace_size(const hga_config* cfg, int32_t max_groups,
                                            int32_t weight, size_t* bytes);

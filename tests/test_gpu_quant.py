@@ -967,3 +967,68 @@ def test_attend_many_routed_groups(dtype, fmt, dim, kg, shared, per_sm):
     assert last - 5 < warps
     if kg >= 400:  # long enough for a slice for most of them
         assert last - 5 >= warps // 2
+
+
+# ---- values and weights far apart
+
+
+def held_bound(it, q, want_lse):
+    """What f16 operands add to `bounds`, per output element.  A weight p s (s: the group's v_scale, or
+    2^(e - 14) for a tail whose largest element is in [2^e, 2^(e + 1))) is two halves, scaled so that
+    the largest one met is at least 2^11: off by half a step of f16's smallest, 2^-25, that is by 2^-36
+    of the largest p s, times the code.  A tail's element below f16's range is off by 2^-39 of
+    the tail's largest, times its weight."""
+    k, v = it.rows("k", range(len(it.k))), it.rows("v", range(len(it.v)))
+    p = np.exp(q @ k.T / np.sqrt(it.dim) - want_lse[:, None])
+    top = np.abs(it.v_tail).max() if len(it.v_tail) else 0.0
+    tail_scale = 2.0 ** (np.floor(np.log2(top)) - 14) if top else 1.0
+    s = np.concatenate([np.repeat([float(x[1]) for x in it.v], 16), np.full(len(it.v_tail), tail_scale)])
+    code = np.abs(v) / np.where(s > 0, s, 1.0)[:, None]
+    tail = p[:, 16 * len(it.v):].sum(1, keepdims=True) * top
+    return 2.0 ** -36 * (p * s).max(1, keepdims=True) * code.sum(0) + 2.0 ** -39 * tail
+
+
+def check_held(c, q, got):
+    out = got[0].double().cpu().numpy()[:, :, 0]
+    torch.cuda.synchronize()
+    assert B.hga_device_status() == 0
+    g = c.hq // c.h
+    for b in range(c.b):
+        for h in range(c.h):
+            it, rows = c.items[b][h], slice(h * g, h * g + g)
+            qq = stored(q[b, rows, 0], c.dtype)
+            want, want_lse, _ = it.attend(qq)
+            tol = bounds(it, qq, None, c.out_kind, want, want_lse)[0] + held_bound(it, qq, want_lse)
+            err = np.abs(out[b, rows] - want)
+            assert (err <= tol).all(), (b, h, np.max(err / tol))
+
+
+@pytest.mark.parametrize("dtype,fmt,shared", [("bf16", "e4m3", 4), ("bf16", "int8", 8), ("f32", "e4m3", 3), ("bf16", "int8", 16)])
+def test_attend_dimensions_that_only_light_groups_feed(dtype, fmt, shared):
+    """Each group's V lives in 16 dimensions of its own, its size 2^0 to 2^-44 from group to group:
+    every dimension is held to what the call documents."""
+    c = Cache(2, 2, 128, 24, dtype, fmt, heads_q=2 * shared, seed=37)
+    k, v = c.rng.standard_normal((2, 2, 2, 370, 128))
+    for g in range(24):
+        own = np.zeros(128)
+        own[16 * (g % 8):16 * (g % 8) + 16] = 2.0 ** -(2 * g if g < 23 else 20)
+        v[:, :, 16 * g:16 * g + 16] *= own
+    c.append(k, v, [370, 352])
+    q = c.q(0.5)
+    check_held(c, q, c.attend(q))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_tail_rows_far_apart(dtype):
+    """Rows of a tail from 2^30 to 2^-30, the weight on a small one: alone, and beside closed
+    groups."""
+    c = Cache(3, 2, 64, 4, dtype, heads_q=6, seed=38)
+    k, v = c.rng.standard_normal((2, 3, 2, 43, 64))
+    size = 2.0 ** c.rng.integers(-30, 31, (3, 2, 43, 1))
+    size[:, :, 32:] = 2.0 ** np.linspace(30, -30, 11)[:, None]
+    size[2, :, :13] = 2.0 ** np.linspace(-30, 30, 13)[:, None]
+    v *= size
+    c.append(k, v, [43, 32, 13])
+    for at in (42, 38, 2):
+        q = 6 * k[:, :, at].repeat(3, axis=1)[:, :, None]
+        check_held(c, q, c.attend(q))
