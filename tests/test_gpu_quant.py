@@ -1032,3 +1032,102 @@ def test_attend_tail_rows_far_apart(dtype):
     for at in (42, 38, 2):
         q = 6 * k[:, :, at].repeat(3, axis=1)[:, :, None]
         check_held(c, q, c.attend(q))
+
+
+# ---- summaries of ragged and of bounded caches, rows of eviction that are read one after the other
+
+
+def built(c, k, n_alloc):
+    """Summary rows that hga_build_summaries makes of all tokens k [B, Hkv, n_alloc, D]."""
+    chunks, per = n_alloc // c.layer.chunk, c.layer.chunk // 16
+    cs = torch.full((c.b, c.h, chunks, c.d), 9.0, device="cuda")
+    gs = torch.full((c.b, c.h, chunks, per, c.d), 9.0, device="cuda")
+    B.hga_build_summaries(c.layer, to_gpu(k, c.dtype), n_alloc, 0, n_alloc, cs, gs)
+    return cs, gs
+
+
+@pytest.mark.parametrize("dtype,fmt,dim,chunk,high", [
+    ("bf16", "e4m3", 128, 64, 32), ("bf16", "int8", 64, 128, 16), ("f32", "int8", 128, 128, 0), ("f32", "e4m3", 64, 64, 32)])
+def test_append_ragged_with_summaries(dtype, fmt, dim, chunk, high):
+    """Padded prompts of different lengths, then pieces of different lengths: each sequence's rows are
+    the batch builder's bits, and no others are written."""
+    n_alloc = 2048
+    c = Cache(6, 2, dim, n_alloc // 16, dtype, fmt, seed=39, chunk=chunk, n_high_pairs=high)
+    k, v = c.rng.standard_normal((2, 6, 2, n_alloc, dim))
+    want_cs, want_gs = built(c, k, n_alloc)
+    cs, gs = torch.full_like(want_cs, 9.0), torch.full_like(want_gs, 9.0)
+    done = np.zeros(6, int)
+    for counts in ([1900, 0, 15, 64, 333, 1024], [1, 17, 1, 65, 128, 0], [100, 300, 0, 700, 1, 1024]):
+        n = max(counts)
+        part = np.full((2, 6, 2, n, dim), np.nan)
+        for b, m in enumerate(counts):
+            part[0, b, :, :m], part[1, b, :, :m] = k[b, :, done[b]:done[b] + m], v[b, :, done[b]:done[b] + m]
+        c.append(part[0], part[1], counts, chunk_sum=cs, group_sum=gs)
+        done += counts
+        c.check_stored()
+        for b in range(6):
+            groups, chunks = done[b] // 16, done[b] // chunk
+            got, want = gs[b].flatten(1, 2), want_gs[b].flatten(1, 2)
+            assert torch.equal(got[:, :groups], want[:, :groups]) and (got[:, groups:] == 9).all()
+            assert torch.equal(cs[b, :, :chunks], want_cs[b, :, :chunks]) and (cs[b, :, chunks:] == 9).all()
+
+
+def test_summaries_of_a_bounded_cache():
+    """After evictions a group's table entry and its summary row are different numbers.  Rows go on
+    being the batch builder's; a group behind the summary tables is flagged, its codes are written."""
+    keep, total = 6, 256
+    c = Cache(2, 2, 64, total // 16, heads_q=2, seed=40, evicts=True, n_high_pairs=16)
+    k, v = c.rng.standard_normal((2, 2, 2, total + 32, 64))
+    want_cs, want_gs = built(c, k[:, :, :total], total)
+    cs, gs = torch.full_like(want_cs, 9.0), torch.full_like(want_gs, 9.0)
+    weight = torch.zeros(2, 2, total // 16, device="cuda")
+    at = 0
+    for n in [100] + [1] * 30 + [37, 5, 16, 64, 4, 16, 16]:
+        c.append(k[:, :, at:at + n], v[:, :, at:at + n], chunk_sum=cs, group_sum=gs)
+        at += n
+        assert B.hga_device_status() == (6 if at // 16 > 16 else 0)  # groups 16 and 17
+        c.attend(c.q(), weight=weight, weight_out=weight)
+        given = weight.cpu().numpy()
+        B.hga_quant_evict(c.layer, c.view(), c.pos_t(), keep, 1, 2, weight, weight, c.table, c.evicted)
+        for b in range(2):
+            for h in range(2):
+                it = c.items[b][h]
+                stay = Q.keep_groups(given[b, h], len(it.k), keep, 1, 2)
+                it.k, it.v = [it.k[i] for i in stay], [it.v[i] for i in stay]
+        c.check_stored()
+    assert at == total + 32 and (c.evicted == 18 - keep).all()
+    assert torch.equal(gs, want_gs) and torch.equal(cs, want_cs)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("keep,sink,recent", [(1, 0, 0), (20000, 4, 64), (29999, 0, 0)])
+def test_evict_rows_beyond_shared_memory(keep, sink, recent, in_place):
+    """Tables of 30,000 entries (weights, then slots, go through shared memory): ragged numbers of
+    groups, weights that tie across the threshold, NaN, open groups, a bad position."""
+    total = 30000
+    rng = np.random.default_rng(keep)
+    ns = [0, 1, keep, keep + 1, 25013, total]
+    c = Cache(len(ns) + 1, 2, 64, total, seed=41, evicts=True)
+    for i, n in enumerate(ns):
+        c.pos[i] = 16 * n + (0 if n == total else 7 * i % 16) - 1
+    c.pos[-1] = 16 * total + 5                        # a group too many
+    w = np.round(rng.standard_normal((len(ns) + 1, 2, total)).astype(np.float32) * 2)  # few different values
+    w[rng.integers(0, 50, w.shape) == 0] = np.nan
+    got_w, got_t, got_e = run_evict(c, torch.tensor(w).cuda(), keep, sink, recent, in_place)
+    assert B.hga_device_status() == 6
+    table = c.table.cpu().numpy()
+    np.testing.assert_array_equal(got_w[-1], w[-1])
+    np.testing.assert_array_equal(got_t[-1], table[-1])
+    assert not got_e[-1].any()
+    for b, n in enumerate(ns):
+        for h in range(2):
+            stay = Q.keep_groups(w[b, h], n, keep, sink, recent)
+            kept = set(stay)
+            freed = [g for g in range(n) if g not in kept]
+            np.testing.assert_array_equal(got_t[b, h], table[b, h, stay + freed + list(range(n, total))])
+            want = np.zeros(total, np.float32)
+            want[:len(stay)] = w[b, h, stay]
+            if n < total:
+                want[len(stay)] = w[b, h, n]
+            np.testing.assert_array_equal(got_w[b, h], want)
+            assert got_e[b, h] == len(freed)
