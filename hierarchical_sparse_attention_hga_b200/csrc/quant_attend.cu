@@ -8,10 +8,11 @@
 // tokens and the G query heads of the KV head, is added to an accumulator.
 //
 // Bound by HBM: 2 D bytes a token are read once, for 4 G D operations.  16 x 32K
-// tokens of 8 KV heads, 4 query heads each: 176 us with the merge, 6.1 TB/s, 0.94 of
-// a copy; 8 heads 180 us; 16 heads 228 us, there by the instructions; 8 x 128K int8
-// 340 us, 375 under sustained load at the power limit.  Few or short items are a chain
-// of latencies: one 1K prompt 8 us, 128 short ones 28 us (11.8 by their bytes).  Each warp
+// tokens of 8 KV heads, 4 query heads each: 178 us with the merge, 6.1 TB/s, 0.93 of
+// a copy; 8 heads 180 us; 16 heads 235 us, there by the instructions; 8 x 128K int8
+// 341 us, 380 under sustained load at the power limit.  Few or short items cost more than
+// their bytes, by the partials and by what each item waits for: one 1K prompt 9 us, one of
+// 32K 22 us (10.3 by its bytes), 128 short ones 28.5 us (11.8).  Each warp
 // streams groups through a ring of its own in shared memory (one TMA box for a
 // group's K, one for its V), reads the codes back in
 // the very bytes that the matrix instruction's operand layout wants from each
@@ -720,7 +721,7 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     skip = 0;
     typename W::Row q_raw[NT][NK];
     w.fetch_q(q, p, b, h, q_raw);  // on its way while the slots are
-    pdl_trigger();  // every CTA of the grid is resident: the merge may take the places they leave
+    pdl_trigger();  // once every CTA has come here or left, the merge may take the places that others leave
     if (lane == 0 && u_lo == 0) {  // this warp has the item's first unit; its last one is total - u_hi further on
       const int me = static_cast<int>(worker()), more = static_cast<int>((static_cast<unsigned>(max(0, -left)) + slice - 1) / slice);
       ws.parts[item] = make_int2(me, min(more, static_cast<int>(gridDim.x) * kWarps - 1 - me) + 1);
