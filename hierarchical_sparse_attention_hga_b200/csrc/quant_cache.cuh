@@ -16,7 +16,8 @@ namespace hga {
 
 constexpr int kQuantGroup = 16;  // tokens per group (cfg group is 16)
 constexpr int kQuantMaxGroups = 1 << 20;  // table entries per (sequence, KV head)
-constexpr int64_t kQuantMaxPos = int64_t{1} << 40;  // positions count evicted tokens too
+// Positions count evicted tokens too; the groups before them fit `evicted`, an int32.
+constexpr int64_t kQuantMaxPos = (int64_t{1} << 35) - 2;
 constexpr int64_t kQuantMaxSlots = (1 << 27) - 1;  // a slot's first row is an int32 coordinate
 
 struct QuantCache {

@@ -123,8 +123,8 @@ typedef enum hga_quant_format { HGA_QUANT_E4M3 = 0, HGA_QUANT_INT8 = 1 } hga_qua
  * the open group (the last (pos + 1) % 16 tokens) are kept unrounded in the
  * tails.  evicted counts the groups hga_quant_evict removed, so the live closed
  * groups of (b, h) at position pos are (pos + 1) / 16 - evicted[b, h]; NULL:
- * none was ever evicted.  Positions count every token that was appended (up to
- * 2^40).  pos[b] == -1 is a sequence with no tokens.
+ * none was ever evicted.  Positions count every token that was appended, and end
+ * at 2^35 - 2, where evicted does.  pos[b] == -1 is a sequence with no tokens.
  */
 typedef struct hga_quant_cache {
   void* k;                /* device 8-bit [n_slots, 16, D], 16-byte aligned */

@@ -1131,3 +1131,37 @@ def test_evict_rows_beyond_shared_memory(keep, sink, recent, in_place):
                 want[len(stay)] = w[b, h, n]
             np.testing.assert_array_equal(got_w[b, h], want)
             assert got_e[b, h] == len(freed)
+
+
+# ---- the last positions
+
+
+def test_positions_end_where_the_count_of_evicted_groups_does():
+    """2^35 - 2 is the last position: the groups before it fit an int32.  The next one is flagged, and
+    an eviction there, whose count would pass 2^31, leaves its item as it is."""
+    c = Cache(2, 2, 64, 8, heads_q=4, seed=42, evicts=True)
+    c.fill([3 * 16 + 14, 7 * 16 + 14])
+    c.evicted[0], c.evicted[1] = 2 ** 31 - 1 - 3, 2 ** 31 - 1 - 7
+    c.pos += 16 * c.evicted[:, 0].cpu().numpy().astype(np.int64)
+    new = c.rng.standard_normal((2, 2, 2, 1, 64))
+    c.append(new[0], new[1])
+    assert (c.pos == 2 ** 35 - 2).all()
+    c.check_stored()
+    q = c.q()
+    weight = torch.rand(2, 2, 8, device="cuda")
+    w_out = torch.full_like(weight, -5)
+    c.check_attend(q, c.attend(q, weight=weight, weight_out=w_out), None, weight, w_out)
+    _, _, got_e = run_evict(c, weight, 2, 0, 1, False)
+    assert (got_e == 2 ** 31 - 3).all() and B.hga_device_status() == 0
+    tail = c.kt.clone()
+    B.hga_quant_append(c.layer, c.view(), to_gpu(new[0], "bf16"), to_gpu(new[1], "bf16"), 1, c.pos_t() + 1)
+    assert B.hga_device_status() == 6 and torch.equal(torch.nan_to_num(c.kt), torch.nan_to_num(tail))
+    c.pos += 16 * 3                                   # as if appended: 2^31 + 2 groups in all
+    c.evicted += 3
+    got_w, got_t, got_e = run_evict(c, weight, 2, 0, 1, False)
+    assert B.hga_device_status() == 6
+    np.testing.assert_array_equal(got_e, c.evicted.cpu().numpy())
+    np.testing.assert_array_equal(got_t, c.table.cpu().numpy())
+    np.testing.assert_array_equal(got_w, weight.cpu().numpy())
+    out, lse = c.attend(q)
+    assert B.hga_device_status() == 6 and not out.any() and torch.isneginf(lse).all()
