@@ -156,10 +156,14 @@ def _ptr(x):
 
 def _dense(x):
     """_ptr of a tensor that has to be contiguous (a slice of a larger one often is not)."""
-    check = getattr(x, "is_contiguous", None)
-    if check is not None and not check():
-        raise ValueError("tensors passed to the library must be contiguous")
-    return _ptr(x)
+    if x is None:
+        return None
+    try:
+        if x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
+    raise ValueError("tensors passed to the library must be contiguous")
 
 
 def _stream(stream):
