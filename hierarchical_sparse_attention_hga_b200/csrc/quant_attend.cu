@@ -564,7 +564,9 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
   // per unit, two blocks of 32: k_scale, v_scale as mantissa and exponent, state (1: in
   // the ring, 0: no tokens, -1: id not kept)
   __shared__ float4 s_units[kWarps][2][32];
-  __shared__ int64_t s_before[kThreads];                // list length before each thread's rows
+  // list length before each thread's rows: used up before the first unit is staged
+  static_assert(kThreads * sizeof(int64_t) <= sizeof(s_units), "where the units will stand");
+  int64_t* s_before = reinterpret_cast<int64_t*>(s_units);
   __shared__ int64_t s_all;
   __shared__ int s_tokens[kThreads];                    // live tokens of each thread's row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -690,7 +692,10 @@ quant_attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
       }
       if (item < items) enter_item();
     }
-    if (waited) break;
+    if (waited) {
+      __syncthreads();  // every warp has searched
+      break;
+    }
     pdl_wait();
     waited = true;
     if (!__syncthreads_or(tid < rows && pos[tid] != seen)) {
@@ -1144,7 +1149,7 @@ cudaError_t launch_attend(const LayerParams& p, const QuantCache& qc, const void
   const int64_t slices = (items * (most + kItemCost) + kMinSlice - 1) / kMinSlice;
   const size_t smem = 1024 + kWarps * (kStages * kTile * Tile<D>::kUnitBytes + (group_idx ? p.kg * sizeof(int) : 0));
   // An SM's 228 KB hold fewer CTAs where there are many routed ids (D = 128, from about
-  // 280 on): slices for CTAs that only come in a second wave would be as long as the others.
+  // 350 on): slices for CTAs that only come in a second wave would be as long as the others.
   static const size_t fixed = [] {
     cudaFuncAttributes a;
     return cudaFuncGetAttributes(&a, quant_attend_kernel<T, D, FORMAT, GM>) == cudaSuccess ? a.sharedSizeBytes : 0;

@@ -935,7 +935,7 @@ def test_attend_reports_a_copy_that_never_comes(lens):
 
 
 @pytest.mark.parametrize("dtype,fmt,dim,kg,shared,per_sm", [
-    ("bf16", "e4m3", 128, 32, 4, 3), ("bf16", "int8", 128, 1024, 4, 2), ("f32", "e4m3", 128, 400, 8, 2),
+    ("bf16", "e4m3", 128, 32, 4, 3), ("bf16", "e4m3", 128, 340, 4, 3), ("bf16", "int8", 128, 1024, 4, 2), ("f32", "e4m3", 128, 400, 8, 2),
     ("f32", "int8", 64, 1024, 3, 3), ("bf16", "e4m3", 128, 1024, 16, 2)])
 def test_attend_many_routed_groups(dtype, fmt, dim, kg, shared, per_sm):
     """Up to 1024 routed groups, which take shared memory from the CTAs: the slices are cut for the
